@@ -36,6 +36,7 @@ __all__ = [
     "scan_fwd_gated", "scan_bwd_gated", "scan_log_fwd_gated", "scan_log_bwd_gated",
     "scan_causal", "scan_bidirectional_branched", "scan_log", "matrix_scan", "GATE_SIGMOID", "GATE_NEG_SOFTPLUS",
     "workspace_bytes", "OP_SCAN_FWD", "OP_SCAN_BWD", "OP_SCAN_LOG_FWD", "OP_MATRIX_FWD", "OP_MATRIX_BWD",
+    "linear_attention_fwd",
     "OP_SCAN_LOG_BWD", "set_debug", "debug_enabled", "workspace_error", "stream_ceiling", "release_capture_workspaces",
 ]
 
@@ -94,6 +95,8 @@ def load_library(path: str):
         "mscan_stream_ceiling": (i32, [ctypes.POINTER(p), i32, ctypes.POINTER(p), i32, sz, p]),
         "mscan_debug_partial_fwd": (i32, [P, i32, i32, p, p, p, p, sz, ctypes.c_int64, ctypes.c_int64, ctypes.c_uint32,
                                           p]),
+        "linear_attention_workspace_bytes": (sz, [p, i32]),
+        "linear_attention_fwd": (i32, [p, i32, p, p, p, p, p, p, p, p, sz, p]),
         "mscan_status_string": (ctypes.c_char_p, [i32]),
         "mscan_last_hip_error": (ctypes.c_char_p, []),
         "mscan_abi_version": (i32, []),
@@ -592,6 +595,12 @@ def matrix_affine_scan_bwd(A, h, dy, h0=None, cu_seqlens=None, reverse=False, ne
         ctypes.byref(prob), k, v, _ptr(A), _ptr(h), _ptr(dy), _ptr(h0), _ptr(dA), _ptr(dB), _ptr(dh0),
         _ptr(ws), ws.numel(), ctypes.c_void_p(sh)), (_ptr(ws), ws.numel(), dev, sh))
     return dA, dB, dh0
+
+
+# ---------------------------------------------------------------------------
+# linear attention (see _attention.py)
+# ---------------------------------------------------------------------------
+from ._attention import linear_attention_fwd  # noqa: E402
 
 
 # ---------------------------------------------------------------------------

@@ -1,0 +1,65 @@
+// Private interface between the C ABI and the linear attention kernels.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace mscan {
+namespace la {
+
+// A [B][T][heads][d] array with a contiguous last axis; head h of the problem
+// reads head h / share.
+struct Heads {
+  const void* p;
+  int64_t sb, st, sh;  // strides in elements
+  int32_t share, d;
+};
+
+struct LaProblem {
+  int64_t B, T;
+  int32_t H, Hk, Dk, Dv;
+  const int32_t* cu;   // packed sequences (B = 1) or null
+  int32_t nseg;        // packed sequences, or B
+  float scale;
+  const float* g;      // log decays, strides in elements
+  int64_t gsb, gst, gsh;
+  // the cut of the time axis (see find_span)
+  int64_t span;        // steps per span, a multiple of 64
+  int32_t spans;       // spans per sequence of an unpacked problem
+  int32_t slots;       // spans of the whole problem
+};
+
+// Steps per span, for LaProblem::span; sets spans and slots too.
+void plan(LaProblem& p, bool backward);
+
+struct FwdArgs {
+  LaProblem pr;
+  Heads q, k, v;
+  void* o;             // [B][T][H][Dv]
+  const float* h0;     // [N][H][Dk][Dv] or null
+  float* ht;           // [N][H][Dk][Dv] or null
+  float* states;       // split problems: [slots][H][Dk][Dv]
+  float* totals;       // split problems: [slots][H], the decay over a span
+};
+hipError_t launch_fwd(const FwdArgs& a, int dtype, hipStream_t st);
+
+struct BwdArgs {
+  LaProblem pr;
+  Heads q, k, v, dO;
+  const float* h0;     // [N][H][Dk][Dv] or null
+  const float* dht;    // or null
+  void *dq, *dk, *dv;  // [B][T][Hk][Dk] x 2, [B][T][H][Dv]
+  float* dg;           // [B][T][H], or [H] when dg_sum, or null
+  bool dg_sum;
+  float* dh0;          // or null
+  // workspace
+  float *states, *totals;   // as in FwdArgs (split problems)
+  float *lams;              // split problems: the adjoint state after each span
+  float *dq_part, *dk_part; // shared heads: [B][T][H][Dk] each
+  float *rows;              // dg: [2][B][T][H], and one value per (slot, head) behind it
+  float *dg_part;           // dg_sum: [B][T][H]
+};
+hipError_t launch_bwd(const BwdArgs& a, int dtype, hipStream_t st);
+
+}  // namespace la
+}  // namespace mscan

@@ -1,0 +1,176 @@
+// Linear attention, forward: whole sequences.
+//
+// A workgroup runs one span of one head chunk by chunk, the state in its
+// accumulators: each of its waves holds 32 columns of the Dk x Dv state, which
+// is at once the accumulator of the update and (split into bf16 pieces) an
+// operand of the product with the queries, and never leaves registers inside a
+// span. Scores of a chunk are shared by the waves through LDS. Few long
+// sequences are cut into several spans; a pass over k and v gives each span's
+// own state first, and k_join turns these into the states before the spans.
+#include "la_core.hpp"
+
+namespace mscan {
+namespace la {
+
+template <class TIn, class TM, int DX, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
+  constexpr int C = kChunk<TM>, DZ = NW * 32, NT = NW * 64, NP = kPiecesP<TM>;
+  __shared__ __align__(16) TM Q[C * DX];
+  __shared__ __align__(16) TM K[C * DX];
+  __shared__ __align__(16) TM V[C * DZ];
+  __shared__ __align__(16) TM P[NP * C * C];
+  __shared__ __align__(16) Decays<C> dec;
+  const LaProblem& pr = a.pr;
+  const int tid = threadIdx.x, wave = tid >> 6, z0 = wave * 32;
+  const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
+  const Span sp = find_span(pr, slot);
+  const int64_t ost = (int64_t)pr.H * pr.Dv;
+  TIn* op = (TIn*)a.o + (sp.batch * pr.T + sp.t0) * ost + (int64_t)h * pr.Dv;
+  if (pr.cu && sp.seq >= pr.nseg) {  // steps behind the last sequence
+    for (int64_t i = tid; i < (int64_t)sp.n * pr.Dv; i += NT) op[i / pr.Dv * ost + i % pr.Dv] = (TIn)0.f;
+    return;
+  }
+  if (sp.n == 0 && !sp.is_last) return;
+  const int64_t cells = (int64_t)pr.Dk * pr.Dv;
+  const float* s_in = sp.is_first ? (a.h0 ? a.h0 + ((int64_t)sp.seq * pr.H + h) * cells : nullptr)
+                                  : a.states + ((int64_t)slot * pr.H + h) * cells;
+  f16v S[DX / 32];
+  load_state<DX>(S, s_in, pr.Dv, 1, pr.Dk, pr.Dv, z0);
+  const TIn* qp = head_base<TIn>(a.q, sp.batch, sp.t0, h);
+  const TIn* kp = head_base<TIn>(a.k, sp.batch, sp.t0, h);
+  const TIn* vp = head_base<TIn>(a.v, sp.batch, sp.t0, h);
+  const float* gp = gate_base(pr, sp.batch, sp.t0, h);
+  TileRegs<TIn, C, DX, NT> rq, rk;
+  TileRegs<TIn, C, DZ, NT> rv;
+  float rg = 0.f;
+  auto fetch = [&](int t) {
+    rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t, tid);
+    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t, tid);
+    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t, tid);
+    if (wave == 0) rg = load_gate(gp, pr.gst, t, sp.n);
+  };
+  fetch(0);
+  for (int t = 0; t < sp.n; t += C) {
+    rq.store(Q, tid);
+    rk.store(K, tid);
+    rv.store(V, tid);
+    if (wave == 0) write_decays<C>(dec, rg);
+    __syncthreads();
+    if (t + C < sp.n) fetch(t + C);
+    scores<TM, C, DX, NP, false>(Q, K, P, dec, pr.scale, wave, NW);
+    f16v acc[C / 32];
+    from_state<TM, C, DX, kPiecesX<TM>>(Q, S, acc);
+    scale_rows<C>(acc, dec.up, pr.scale);
+    __syncthreads();
+    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(K, V, P, dec, 1.f, z0, S, acc);
+    store_rows<TIn, C>(acc, op + t * ost, ost, sp.n - t, pr.Dv, z0);
+    __syncthreads();
+  }
+  if (sp.is_last && a.ht)
+    store_state<DX>(S, a.ht + ((int64_t)sp.seq * pr.H + h) * cells, pr.Dv, 1, pr.Dk, pr.Dv, z0);
+}
+
+// The states between the spans of a sequence: states[slot] holds what a span
+// adds and becomes what the recurrence brings to its start (REV: to its end,
+// from the last span to the first).
+template <bool REV>
+__global__ __launch_bounds__(256) void k_join(const LaProblem pr, const float* outer, float* states,
+                                              const float* totals) {
+  const int64_t cells = (int64_t)pr.Dk * pr.Dv;
+  const int parts = (int)((cells / 4 + 255) / 256);
+  const int part = blockIdx.x % parts, h = blockIdx.x / parts % pr.H, seq = blockIdx.x / parts / pr.H;
+  const int64_t at = ((int64_t)part * 256 + threadIdx.x) * 4;
+  if (at >= cells) return;
+  int64_t first, len;
+  if (pr.cu) {
+    const int64_t start = clamp_cu(pr, seq);
+    first = start / pr.span + seq;
+    len = clamp_cu(pr, seq + 1) - start;
+  } else {
+    first = (int64_t)seq * pr.spans;
+    len = pr.T;
+  }
+  const int n = (int)((len + pr.span - 1) / pr.span);
+  f4v S = {0.f, 0.f, 0.f, 0.f};
+  if (outer) S = *(const f4v*)(outer + ((int64_t)seq * pr.H + h) * cells + at);
+  // four spans' states are in flight at a time
+  for (int c0 = 0; c0 < n; c0 += 4) {
+    f4v add[4];
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c0 + i < n - 1) {
+        const int64_t slot = first + (REV ? n - 1 - (c0 + i) : c0 + i);
+        add[i] = *(const f4v*)(states + (slot * pr.H + h) * cells + at);
+        f[i] = totals[slot * pr.H + h];
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c0 + i < n) {
+        const int64_t slot = first + (REV ? n - 1 - (c0 + i) : c0 + i);
+        *(f4v*)(states + (slot * pr.H + h) * cells + at) = S;
+        if (c0 + i < n - 1) S = S * f[i] + add[i];
+      }
+  }
+}
+
+hipError_t launch_join(const LaProblem& p, bool rev, const float* outer, float* states, const float* totals,
+                       hipStream_t st) {
+  const int64_t cells = (int64_t)p.Dk * p.Dv;
+  const int64_t blocks = (cells / 4 + 255) / 256 * p.H * (p.cu ? p.nseg : p.B);
+  if (rev)
+    hipLaunchKernelGGL((k_join<true>), dim3((unsigned)blocks), dim3(256), 0, st, p, outer, states, totals);
+  else
+    hipLaunchKernelGGL((k_join<false>), dim3((unsigned)blocks), dim3(256), 0, st, p, outer, states, totals);
+  return hipGetLastError();
+}
+
+// Steps per span. A workgroup per head and sequence needs no second pass over
+// k and v, but fills the card only with many heads and sequences.
+void plan(LaProblem& p, bool backward) {
+  const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H;
+  const int64_t want = 768 / rows > 0 ? 768 / rows : 1;  // spans per row
+  int64_t span = (p.T + want - 1) / want;
+  span = (span + 63) / 64 * 64;
+  if (span < 256) span = 256;
+  p.span = span;
+  if (p.cu) {
+    p.spans = 0;
+    p.slots = (int32_t)(p.T / span + p.nseg + 1);
+  } else {
+    p.spans = (int32_t)((p.T + span - 1) / span);
+    p.slots = (int32_t)(p.B * p.spans);
+  }
+}
+
+template <class TIn, class TM, int DX, int NW>
+static hipError_t fwd_dims(const FwdArgs& a, hipStream_t st) {
+  const unsigned blocks = (unsigned)((int64_t)a.pr.slots * a.pr.H);
+  if (a.pr.T > a.pr.span) {
+    hipLaunchKernelGGL((k_span_states<TIn, TM, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, a.pr, a.k, a.v,
+                       1.f, a.states, a.totals);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    if ((e = launch_join(a.pr, false, a.h0, a.states, a.totals, st)) != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL((k_attn_fwd<TIn, TM, DX, NW>), dim3(blocks), dim3(NW * 64), 0, st, a);
+  return hipGetLastError();
+}
+
+template <class TIn, class TM>
+static hipError_t fwd_type(const FwdArgs& a, hipStream_t st) {
+  const bool dk64 = a.pr.Dk <= 64, dv64 = a.pr.Dv <= 64;
+  if (dk64 && dv64) return fwd_dims<TIn, TM, 64, 2>(a, st);
+  if (dk64) return fwd_dims<TIn, TM, 64, 4>(a, st);
+  if (dv64) return fwd_dims<TIn, TM, 128, 2>(a, st);
+  return fwd_dims<TIn, TM, 128, 4>(a, st);
+}
+
+hipError_t launch_fwd(const FwdArgs& a, int dtype, hipStream_t st) {
+  if (dtype == 0) return fwd_type<float, float>(a, st);
+  if (dtype == 1) return fwd_type<__bf16, __bf16>(a, st);
+  return fwd_type<_Float16, float>(a, st);
+}
+
+}  // namespace la
+}  // namespace mscan

@@ -13,15 +13,19 @@
 #include "mscan_launch.hpp"
 
 namespace {
-
 thread_local char g_last_hip_error[256] = "";
+}  // namespace
 
-mscan_status hip_status(hipError_t e) {
+int mscan::status_of_hip(hipError_t e) {
   if (e == hipSuccess) return MSCAN_OK;
   strncpy(g_last_hip_error, hipGetErrorString(e), sizeof(g_last_hip_error) - 1);
   g_last_hip_error[sizeof(g_last_hip_error) - 1] = '\0';
   return MSCAN_ERR_HIP;
 }
+
+namespace {
+
+mscan_status hip_status(hipError_t e) { return (mscan_status)mscan::status_of_hip(e); }
 
 bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
 

@@ -6,6 +6,9 @@
 
 namespace mscan {
 
+// The mscan status of a HIP error, whose text mscan_last_hip_error() then gives.
+int status_of_hip(hipError_t e);
+
 // Arguments of the scalar forward / backward kernels (see scan_scalar.hip).
 struct ScalarArgs {
   const void* g;        // gates, fp32 or bf16

@@ -236,6 +236,60 @@ MSCAN_API mscan_status matrix_affine_scan_bwd(const mscan_problem* prob, int k, 
                                     const float* h, const float* dy, const float* h0, float* dA,
                                     float* dB, float* dh0, void* ws, size_t ws_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Linear attention with a decay for each head: the same recurrence with an
+ * outer product as injection and a query that reads the state,
+ *   S_t = e^{g_t} S_{t-1} + k_t v_t^T        (S: Dk x Dv per head and sequence)
+ *   o_t = scale * S_t^T q_t.
+ *
+ *  Types.     q, k, v, o and their gradients share one dtype (MSCAN_F32,
+ *             MSCAN_BF16 or MSCAN_F16). Log decays, states and their gradients
+ *             are fp32. Sums, decays and states are held in fp32 (log decays
+ *             are added up in fp64); bf16 products run on the matrix cores with
+ *             every fp32 operand split into bf16 pieces, so states and gate
+ *             gradients keep fp32 precision. Results are bit-reproducible.
+ *  Layout.    q, k: [B][T][Hk][Dk], v: [B][T][H][Dv], strided
+ *             (mscan_heads), last axis contiguous, 16-byte aligned pointers and
+ *             strides of whole 16 bytes. H is a multiple of Hk; head h reads
+ *             queries and keys of head h / (H / Hk). Dk and Dv are multiples of
+ *             8 up to 128. o, dv: [B][T][H][Dv], dq, dk: [B][T][Hk][Dk],
+ *             contiguous.
+ *  Decays.    g: fp32, element (b, t, h) at b*g_strides[0] + t*g_strides[1] +
+ *             h*g_strides[2]; zero strides share a decay. -inf is a reset
+ *             (e^g = 0; so is any g below -1e5).
+ *  Sequences. cu_seqlens as above with B = 1; else NULL, nseg = B, and every
+ *             batch entry is one sequence of T steps. Steps behind
+ *             cu_seqlens[nseg] get outputs and gradients of zero. A NaN or an
+ *             infinity stays in its sequence; inside it, it can reach the
+ *             outputs of up to 63 steps before it.
+ *  States.    h0, ht, dht, dh0: [nseg][H][Dk][Dv], contiguous, 16-byte
+ *             aligned; NULL h0 is zero. An empty sequence has ht = h0.
+ *  Errors, stream and workspace as above; the workspace's contents do not
+ *  matter and nothing is kept in it between calls.                          */
+typedef struct {
+  int64_t B, T;               /* batch entries and steps of each, T <= 2^31 - 1 */
+  int32_t H, Hk, Dk, Dv;
+  const int32_t* cu_seqlens;  /* device, nseg + 1 offsets, or NULL              */
+  int32_t nseg;
+  float scale;
+  int64_t g_strides[3];
+} mscan_attention;
+
+typedef struct {
+  const void* p;
+  int64_t strides[3];         /* batch, step, head, in elements                 */
+} mscan_heads;
+
+/* Workspace bytes of linear_attention_fwd (backward = 0) or _bwd (1); pure host
+ * function, 0 for an invalid problem. */
+MSCAN_API size_t linear_attention_workspace_bytes(const mscan_attention* prob, int backward);
+
+/* o and, if ht is not NULL, the state after each sequence. */
+MSCAN_API mscan_status linear_attention_fwd(const mscan_attention* prob, int dtype, const mscan_heads* q,
+                                            const mscan_heads* k, const mscan_heads* v, const float* g,
+                                            const float* h0, void* o, float* ht, void* ws, size_t ws_bytes,
+                                            void* stream);
+
 /* Measurement aid (not part of the scan): the practical HBM ceiling for a
  * kernel that reads nsrc arrays and writes ndst arrays of n floats each. It
  * streams exactly those bytes with the scan kernels' access type

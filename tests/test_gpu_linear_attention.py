@@ -1,0 +1,195 @@
+"""Linear attention on the GPU against the recurrence in 64 bits.
+
+Tolerances. With M the result's sum over absolute values (attention_reference):
+ - an fp32 sum of n terms is off by at most n 2^-24 M; the chunked form adds each
+   term into a state (T steps), a product over Dk or Dv and one over a chunk. A
+   decay e^x is off by |x| 2^-24 from the rounding of x plus 2^-23, and counts
+   only while e^x does: |x| e^x stays below the factor's own share. So
+   fp32 = (T + Dk + Dv + 256) 2^-24 M;
+ - bf16 operands: the pieces of scores and states leave 2^-17 M in o, dq, dk, dv
+   (2 pieces of 8 bits each, one rounding each);
+ - the output's own rounding: eps / 2 of the value.
+"""
+import numpy as np
+import pytest
+import torch
+
+import attention_reference as ref
+
+pytestmark = pytest.mark.gpu
+DEV = "cuda:0"
+TYPES = {"bf16": torch.bfloat16, "fp16": torch.float16, "fp32": torch.float32}
+
+
+@pytest.fixture(scope="module")
+def m():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    import associative_scan_amd as m
+    return m
+
+
+def f64(t):
+    return None if t is None else t.detach().double().cpu().numpy()
+
+
+def make(seed, B, T, H, Dk, Dv, dtype="bf16", Hk=None, gate="token", n=None, spread=(1.0, 6.0)):
+    """q, k, v, g, h0, do, dht on the GPU."""
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(seed)
+    r = lambda *s: torch.randn(s, device=DEV, generator=gen)  # noqa: E731
+    dt, Hk, n = TYPES[dtype], Hk or H, n or B
+    far = torch.linspace(*spread, H, device=DEV)
+    g = torch.nn.functional.logsigmoid(r(B, T, H) + far if gate == "token" else far)
+    return (r(B, T, Hk, Dk).to(dt), r(B, T, Hk, Dk).to(dt), r(B, T, H, Dv).to(dt), g, r(n, H, Dk, Dv),
+            r(B, T, H, Dv).to(dt), r(n, H, Dk, Dv))
+
+
+def close(got, want, name, T, Dk, Dv, dtype):
+    val, mag = want
+    got64 = f64(got)
+    assert got64.shape == val.shape, (name, got64.shape, val.shape)
+    tol = (T + Dk + Dv + 256) * 2.0 ** -24 * mag + 1e-30
+    if got.dtype != torch.float32:
+        tol = tol + torch.finfo(got.dtype).eps / 2 * np.abs(val)
+        tol = tol + torch.finfo(got.dtype).tiny  # fp16's subnormals: half a step of 2^-24
+    if dtype == "bf16" and name in ("o", "dq", "dk", "dv"):
+        tol = tol + 2.0 ** -17 * mag
+    off = np.abs(got64 - val)
+    assert np.all(np.isfinite(got64)), name
+    worst = float(np.max(off / tol)) if off.size else 0.0
+    assert worst <= 1.0, f"{name}: {worst:.2f} of the tolerance"
+
+
+def check_forward(m, x, cu=None, scale=None, h0=True, dtype="bf16"):
+    q, k, v, g, s0 = x[:5]
+    s0 = s0 if h0 else None
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV)
+    o, ht = m.linear_attention_fwd(q, k, v, g, h0=s0, cu_seqlens=c, scale=scale)
+    sc = q.shape[3] ** -0.5 if scale is None else scale
+    wo, wh = ref.forward(f64(q), f64(k), f64(v), f64(g), f64(s0), cu, sc)
+    d = (q.shape[1], q.shape[3], v.shape[3], dtype)
+    close(o, wo, "o", *d)
+    close(ht, wh, "ht", *d)
+    return o, ht
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T", [1, 2, 31, 32, 33, 63, 64, 65, 127, 130, 255, 256, 257, 600])
+def test_forward_lengths(m, T, dtype):
+    check_forward(m, make(T, 2, T, 3, 64, 64, dtype), dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("Dk,Dv", [(8, 8), (16, 40), (40, 16), (64, 128), (128, 64), (72, 96), (96, 72), (128, 128),
+                                   (120, 104), (8, 128), (128, 8)])
+def test_forward_head_sizes(m, Dk, Dv, dtype):
+    check_forward(m, make(Dk + Dv, 1, 300, 2, Dk, Dv, dtype), dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_forward_shared_heads_and_head_decays(m, dtype):
+    check_forward(m, make(1, 2, 150, 6, 64, 32, dtype, Hk=2), dtype=dtype)
+    check_forward(m, make(2, 1, 700, 4, 128, 64, dtype, Hk=1, gate="head"), dtype=dtype, h0=False, scale=0.5)
+
+
+CUTS = [
+    [0, 300],
+    [0, 0, 300],
+    [0, 300, 300],
+    [0, 1, 2, 64, 128, 129, 300],
+    [0, 0, 0, 7, 7, 263, 300, 300],
+    [0, 255, 256, 300],
+]
+
+
+@pytest.mark.parametrize("cu", CUTS, ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_forward_packed(m, cu, dtype):
+    check_forward(m, make(len(cu), 1, 300, 2, 64, 64, dtype, n=len(cu) - 1), cu=cu, dtype=dtype)
+
+
+def test_forward_packed_many_spans(m):
+    cu = [0, 900, 900, 901, 1300, 2600, 2601]
+    check_forward(m, make(5, 1, 2601, 2, 128, 128, n=6, spread=(3.0, 9.0)), cu=cu)
+
+
+def test_forward_spans(m):
+    """Sequences cut into several spans, with memories across all of them."""
+    check_forward(m, make(6, 2, 1500, 2, 128, 128, spread=(4.0, 12.0)))
+    check_forward(m, make(7, 1, 1025, 1, 64, 64, "fp32", spread=(8.0, 8.0)), dtype="fp32")
+
+
+def test_resets(m):
+    """g = -inf and very strong decays: nothing before them is left, and no NaN appears."""
+    q, k, v, g, h0, do, dht = make(8, 1, 200, 2, 64, 64)
+    g[:, 0] = -float("inf")
+    g[:, 63:66] = -float("inf")
+    g[:, 100] = -1e30
+    g[:, 101] = -200.0
+    o, ht = check_forward(m, (q, k, v, g, h0))
+    a, ha = m.linear_attention_fwd(q[:, 100:].contiguous(), k[:, 100:].contiguous(), v[:, 100:].contiguous(),
+                                   g[:, 100:].contiguous())
+    assert torch.allclose(o[:, 100:].float(), a.float(), rtol=2 ** -7, atol=1e-3)
+    g[:] = -float("inf")
+    check_forward(m, (q, k, v, g, h0))
+
+
+def test_nan_stays_in_its_sequence(m):
+    cu = [0, 70, 150, 300]
+    q, k, v, g, h0, do, dht = make(9, 1, 300, 2, 64, 64, n=3)
+    c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    o, ht = m.linear_attention_fwd(q, k, v, g, h0=h0, cu_seqlens=c)
+    for bad in (float("nan"), float("inf")):
+        q2, k2, v2, g2, h2 = (x.clone() for x in (q, k, v, g, h0))
+        for x in (q2, k2, v2, g2):
+            x[:, 75:149] = bad
+        h2[1] = bad
+        o2, ht2 = m.linear_attention_fwd(q2, k2, v2, g2, h0=h2, cu_seqlens=c)
+        for s, e, n in ((0, 70, 0), (150, 300, 2)):
+            assert torch.equal(o2[:, s:e], o[:, s:e]) and torch.equal(ht2[n], ht[n])
+        assert torch.isnan(o2[:, 75:149]).any()
+
+
+def test_steps_behind_the_last_sequence_are_zero(m):
+    q, k, v, g, h0, do, dht = make(10, 1, 700, 2, 64, 64, n=2)
+    q[:, 310:] = float("nan")
+    c = torch.tensor([0, 300, 310], dtype=torch.int32, device=DEV)
+    o, ht = m.linear_attention_fwd(q, k, v, g, h0=h0, cu_seqlens=c)
+    assert torch.equal(o[:, 310:], torch.zeros_like(o[:, 310:])) and torch.isfinite(o).all()
+    w, wh = m.linear_attention_fwd(q[:, :310], k[:, :310], v[:, :310], g[:, :310], h0=h0, cu_seqlens=c)
+    assert torch.equal(o[:, :310], w) and torch.equal(ht, wh)
+
+
+def test_strides(m):
+    """Head-major tensors, slices of one projection, broadcast inputs."""
+    q, k, v, g, h0, do, dht = make(11, 2, 140, 4, 64, 32)
+    o, ht = m.linear_attention_fwd(q, k, v, g, h0=h0)
+    hm = lambda x: x.transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
+    o2, ht2 = m.linear_attention_fwd(hm(q), hm(k), hm(v), g.transpose(1, 2).contiguous().transpose(1, 2), h0=h0)
+    assert torch.equal(o, o2) and torch.equal(ht, ht2)
+    both = torch.cat([q, k, torch.cat([v, v], 3)], 2)
+    o3, ht3 = m.linear_attention_fwd(both[:, :, :4], both[:, :, 4:8], both[:, :, 8:, :32], g, h0=h0)
+    assert torch.equal(o, o3) and torch.equal(ht, ht3)
+    kb = k[:1, :, :1].expand(2, 140, 4, 64)
+    o4, ht4 = m.linear_attention_fwd(q, kb, v, g, h0=h0)
+    o5, ht5 = m.linear_attention_fwd(q, kb.contiguous(), v, g, h0=h0)
+    assert torch.equal(o4, o5) and torch.equal(ht4, ht5)
+
+
+def test_repeatable_and_without_final_state(m):
+    q, k, v, g, h0, do, dht = make(12, 2, 2100, 3, 128, 128)
+    o, ht = m.linear_attention_fwd(q, k, v, g, h0=h0)
+    for _ in range(3):
+        o2, ht2 = m.linear_attention_fwd(q, k, v, g, h0=h0)
+        assert torch.equal(o, o2) and torch.equal(ht, ht2)
+    o3, none = m.linear_attention_fwd(q, k, v, g, h0=h0, need_ht=False)
+    assert none is None and torch.equal(o, o3)
+
+
+def test_empty_shapes(m):
+    z = lambda *s: torch.zeros(s, device=DEV, dtype=torch.bfloat16)  # noqa: E731
+    h0 = torch.randn(2, 3, 8, 16, device=DEV)
+    o, ht = m.linear_attention_fwd(z(2, 0, 3, 8), z(2, 0, 3, 8), z(2, 0, 3, 16), torch.zeros(3, device=DEV), h0=h0)
+    assert o.shape == (2, 0, 3, 16) and torch.equal(ht, h0)
+    o, ht = m.linear_attention_fwd(z(0, 5, 3, 8), z(0, 5, 3, 8), z(0, 5, 3, 16), torch.zeros(3, device=DEV))
+    assert o.shape == (0, 5, 3, 16) and ht.shape == (0, 3, 8, 16)
