@@ -7,6 +7,7 @@
 #include "la_launch.hpp"
 #include "mscan.h"
 #include "mscan_launch.hpp"
+#include "qk_norm_rope.hpp"
 
 namespace {
 
@@ -80,6 +81,41 @@ FwdSpace fwd_space(const LaProblem& r) {
   return w;
 }
 
+mscan_status check_norm(const mscan_norm_rope* p, int dtype) {
+  if (!p) return MSCAN_ERR_INVALID;
+  if (dtype != MSCAN_F32 && dtype != MSCAN_BF16 && dtype != MSCAN_F16) return MSCAN_ERR_UNSUPPORTED;
+  if (p->w_dtype != MSCAN_F32 && p->w_dtype != MSCAN_BF16 && p->w_dtype != MSCAN_F16) return MSCAN_ERR_UNSUPPORTED;
+  if (p->B < 1 || p->T < 1 || p->Hq < 1 || p->Hk < 1 || p->D < 1 || p->rot < 0 || p->rot > p->D) return MSCAN_ERR_INVALID;
+  if (p->D % 8 || p->D > 256 || p->rot % 16) return MSCAN_ERR_UNSUPPORTED;
+  const int64_t most = (int64_t)1 << 26;
+  if (p->B > most || p->T > most || p->Hq > most || p->Hk > most || p->B * p->T > most / ((int64_t)p->Hq + p->Hk))
+    return MSCAN_ERR_UNSUPPORTED;
+  if (p->rot && (!p->cos || !p->sin || !aligned16(p->cos) || !aligned16(p->sin) || p->table < 1)) return MSCAN_ERR_INVALID;
+  if ((uintptr_t)p->positions & (p->positions_int64 ? 7u : 3u)) return MSCAN_ERR_INVALID;
+  if (!(p->eps >= 0.f)) return MSCAN_ERR_INVALID;
+  return MSCAN_OK;
+}
+
+mscan::la::NormProblem norm_problem(const mscan_norm_rope* p) {
+  mscan::la::NormProblem r{};
+  r.B = p->B;
+  r.T = p->T;
+  r.D = p->D;
+  r.rot = p->rot;
+  r.interleaved = p->interleaved != 0;
+  r.eps = p->eps;
+  r.cos = p->cos;
+  r.sin = p->sin;
+  r.table = p->table;
+  r.positions = p->positions;
+  r.positions64 = p->positions_int64 != 0;
+  r.per_batch = p->positions_per_batch != 0;
+  r.wtype = p->w_dtype;
+  return r;
+}
+
+bool weight_aligned(const void* w, int dtype) { return ((uintptr_t)w & (dtype == MSCAN_F32 ? 3u : 1u)) == 0; }
+
 }  // namespace
 
 extern "C" {
@@ -114,6 +150,87 @@ mscan_status linear_attention_fwd(const mscan_attention* prob, int dtype, const 
   a.states = w.bytes ? (float*)((char*)ws + w.states) : nullptr;
   a.totals = w.bytes ? (float*)((char*)ws + w.totals) : nullptr;
   return hip_status(mscan::la::launch_fwd(a, dtype, (hipStream_t)stream));
+}
+
+mscan_status linear_attention_step(const mscan_attention* prob, int dtype, const mscan_heads* q, const mscan_heads* k,
+                                   const mscan_heads* v, const float* g, const int32_t* slots, int32_t pool,
+                                   float* state, void* o, void* stream) {
+  mscan_status s = check(prob);
+  if (s != MSCAN_OK) return s;
+  if (dtype != MSCAN_F32 && dtype != MSCAN_BF16 && dtype != MSCAN_F16) return MSCAN_ERR_UNSUPPORTED;
+  if (prob->T != 1 || prob->cu_seqlens || pool < 1 || (!slots && prob->B > pool)) return MSCAN_ERR_INVALID;
+  if (!g || ((uintptr_t)g & 3u) || ((uintptr_t)slots & 3u)) return MSCAN_ERR_INVALID;
+  if (!state || !aligned16(state) || !o || !aligned16(o)) return MSCAN_ERR_INVALID;
+  mscan::la::StepArgs a{};
+  const int share = prob->H / prob->Hk;
+  if ((s = heads(q, dtype, share, prob->Dk, a.q)) != MSCAN_OK) return s;
+  if ((s = heads(k, dtype, share, prob->Dk, a.k)) != MSCAN_OK) return s;
+  if ((s = heads(v, dtype, 1, prob->Dv, a.v)) != MSCAN_OK) return s;
+  if (prob->B * (int64_t)prob->H * ((prob->Dv + 31) / 32) > kMaxBlocks) return MSCAN_ERR_UNSUPPORTED;
+  a.B = (int32_t)prob->B;
+  a.H = prob->H;
+  a.Hk = prob->Hk;
+  a.Dk = prob->Dk;
+  a.Dv = prob->Dv;
+  a.pool = pool;
+  a.scale = prob->scale;
+  a.g = g;
+  a.gsb = prob->g_strides[0];
+  a.gsh = prob->g_strides[2];
+  a.slots = slots;
+  a.state = state;
+  a.o = o;
+  return hip_status(mscan::la::launch_step(a, dtype, (hipStream_t)stream));
+}
+
+mscan_status qk_norm_rope_fwd(const mscan_norm_rope* prob, int dtype, const mscan_heads* q, const mscan_heads* k,
+                              const void* wq, const void* wk, void* yq, void* yk, void* stream) {
+  mscan_status s = check_norm(prob, dtype);
+  if (s != MSCAN_OK) return s;
+  mscan::la::NormSide a{}, b{};
+  if ((s = heads(q, dtype, 1, prob->D, a.x)) != MSCAN_OK) return s;
+  if ((s = heads(k, dtype, 1, prob->D, b.x)) != MSCAN_OK) return s;
+  if (!yq || !yk || !aligned16(yq) || !aligned16(yk)) return MSCAN_ERR_INVALID;
+  if (!weight_aligned(wq, prob->w_dtype) || !weight_aligned(wk, prob->w_dtype)) return MSCAN_ERR_INVALID;
+  a.heads = prob->Hq;
+  a.w = wq;
+  a.y = yq;
+  b.heads = prob->Hk;
+  b.w = wk;
+  b.y = yk;
+  return hip_status(mscan::la::launch_norm(norm_problem(prob), a, b, dtype, false, nullptr, nullptr, nullptr,
+                                           (hipStream_t)stream));
+}
+
+size_t qk_norm_rope_workspace_bytes(const mscan_norm_rope* prob) {
+  if (check_norm(prob, MSCAN_F32) != MSCAN_OK) return 0;
+  unsigned qb, kb;
+  mscan::la::norm_bwd_blocks(norm_problem(prob), prob->Hq, prob->Hk, qb, kb);
+  return ((size_t)qb + kb) * prob->D * 4;
+}
+
+mscan_status qk_norm_rope_bwd(const mscan_norm_rope* prob, int dtype, const mscan_heads* q, const mscan_heads* k,
+                              const void* wq, const void* wk, const mscan_heads* dyq, const mscan_heads* dyk, void* dq,
+                              void* dk, float* dwq, float* dwk, void* ws, size_t ws_bytes, void* stream) {
+  mscan_status s = check_norm(prob, dtype);
+  if (s != MSCAN_OK) return s;
+  mscan::la::NormSide a{}, b{};
+  if ((s = heads(q, dtype, 1, prob->D, a.x)) != MSCAN_OK) return s;
+  if ((s = heads(k, dtype, 1, prob->D, b.x)) != MSCAN_OK) return s;
+  if ((s = heads(dyq, dtype, 1, prob->D, a.dy)) != MSCAN_OK) return s;
+  if ((s = heads(dyk, dtype, 1, prob->D, b.dy)) != MSCAN_OK) return s;
+  if (!dq || !dk || !aligned16(dq) || !aligned16(dk)) return MSCAN_ERR_INVALID;
+  if (((uintptr_t)dwq & 3u) || ((uintptr_t)dwk & 3u)) return MSCAN_ERR_INVALID;
+  if (!weight_aligned(wq, prob->w_dtype) || !weight_aligned(wk, prob->w_dtype)) return MSCAN_ERR_INVALID;
+  if (!ws || !aligned16(ws) || ws_bytes < qk_norm_rope_workspace_bytes(prob)) return MSCAN_ERR_WORKSPACE;
+  a.heads = prob->Hq;
+  a.w = wq;
+  a.y = dq;
+  b.heads = prob->Hk;
+  b.w = wk;
+  b.y = dk;
+  return hip_status(mscan::la::launch_norm(norm_problem(prob), a, b, dtype, true, dwq, dwk, (float*)ws,
+                                           (hipStream_t)stream));
 }
 
 }  // extern "C"

@@ -43,6 +43,19 @@ struct FwdArgs {
 };
 hipError_t launch_fwd(const FwdArgs& a, int dtype, hipStream_t st);
 
+// One step of B sequences against a pool of states.
+struct StepArgs {
+  int32_t B, H, Hk, Dk, Dv, pool;
+  float scale;
+  Heads q, k, v;         // [B][heads][d] (st unused)
+  const float* g;
+  int64_t gsb, gsh;
+  const int32_t* slots;  // [B], or null: row b uses state b
+  float* state;          // [pool][H][Dk][Dv]
+  void* o;               // [B][H][Dv]
+};
+hipError_t launch_step(const StepArgs& a, int dtype, hipStream_t st);
+
 struct BwdArgs {
   LaProblem pr;
   Heads q, k, v, dO;

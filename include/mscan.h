@@ -290,6 +290,58 @@ MSCAN_API mscan_status linear_attention_fwd(const mscan_attention* prob, int dty
                                             const float* h0, void* o, float* ht, void* ws, size_t ws_bytes,
                                             void* stream);
 
+/* One step of prob->B sequences (T = 1, nseg = B, cu_seqlens NULL) against a
+ * pool of states, [pool][H][Dk][Dv] fp32, updated in place:
+ *   S = e^{g_b} S + k_b v_b^T, o_b = scale S^T q_b, S = state[slots[b]].
+ *   q, k, v : [B][heads][d], strides[1] unused; o : [B][H][Dv], written.
+ *   slots   : device, int32 [B], or NULL (row b has state b; B <= pool). A row
+ *             whose slot lies outside [0, pool) is padding: its output is zero
+ *             and no state changes. Rows that share a slot are consecutive
+ *             steps of one sequence, in the order of the batch.
+ *   Other states of the pool are left as they were. No workspace.             */
+MSCAN_API mscan_status linear_attention_step(const mscan_attention* prob, int dtype, const mscan_heads* q,
+                                             const mscan_heads* k, const mscan_heads* v, const float* g,
+                                             const int32_t* slots, int32_t pool, float* state, void* o,
+                                             void* stream);
+
+/* RMS norm of queries and keys for each head with the position rotation, the
+ * step that makes the q and k of linear_attention_fwd out of a projection:
+ *   n = x w / sqrt(mean(x^2) + eps) over the D entries of a head; the first `rot`
+ *   entries of n are rotated in pairs, (a, b) -> (a c - b s, b c + a s), with c
+ *   and s of the token's position: pair i is entries (i, i + rot / 2), or
+ *   (2 i, 2 i + 1) when interleaved.
+ *  q: [B][T][Hq][D], k: [B][T][Hk][D], strided as for linear attention; results
+ *  [B][T][heads][D], contiguous. D is a multiple of 8 up to 256, rot a multiple
+ *  of 16 up to D (0: no rotation; cos, sin and positions are then unused).
+ *  cos, sin: fp32 [table][rot / 2], 16-byte aligned. positions: int32 or int64,
+ *  [T] or [B][T], NULL for 0, 1, ..; outside [0, table) they are clamped.
+ *  wq, wk: [D] of w_dtype, or NULL for ones. fp32 inside, one rounding at the
+ *  end. At most 2^26 rows (tokens times heads) in one call.                   */
+typedef struct {
+  int64_t B, T;
+  int32_t Hq, Hk, D, rot;
+  int32_t interleaved;
+  float eps;
+  const float *cos, *sin;
+  int64_t table;
+  const void* positions;
+  int32_t positions_int64;     /* 0: int32, 1: int64                            */
+  int32_t positions_per_batch; /* 0: [T], 1: [B][T]                             */
+  int32_t w_dtype;
+} mscan_norm_rope;
+
+MSCAN_API mscan_status qk_norm_rope_fwd(const mscan_norm_rope* prob, int dtype, const mscan_heads* q,
+                                        const mscan_heads* k, const void* wq, const void* wk, void* yq, void* yk,
+                                        void* stream);
+
+/* Adjoint: dq, dk (dtype, contiguous) for the results' gradients dyq, dyk
+ * (strided), and dwq, dwk: fp32 [D] or NULL. Bit-reproducible.              */
+MSCAN_API size_t qk_norm_rope_workspace_bytes(const mscan_norm_rope* prob);
+MSCAN_API mscan_status qk_norm_rope_bwd(const mscan_norm_rope* prob, int dtype, const mscan_heads* q,
+                                        const mscan_heads* k, const void* wq, const void* wk, const mscan_heads* dyq,
+                                        const mscan_heads* dyk, void* dq, void* dk, float* dwq, float* dwk, void* ws,
+                                        size_t ws_bytes, void* stream);
+
 /* Measurement aid (not part of the scan): the practical HBM ceiling for a
  * kernel that reads nsrc arrays and writes ndst arrays of n floats each. It
  * streams exactly those bytes with the scan kernels' access type
