@@ -36,7 +36,7 @@ __all__ = [
     "scan_fwd_gated", "scan_bwd_gated", "scan_log_fwd_gated", "scan_log_bwd_gated",
     "scan_causal", "scan_bidirectional_branched", "scan_log", "matrix_scan", "GATE_SIGMOID", "GATE_NEG_SOFTPLUS",
     "workspace_bytes", "OP_SCAN_FWD", "OP_SCAN_BWD", "OP_SCAN_LOG_FWD", "OP_MATRIX_FWD", "OP_MATRIX_BWD",
-    "linear_attention_fwd", "linear_attention_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
+    "linear_attention_fwd", "linear_attention_bwd", "linear_attention_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
     "OP_SCAN_LOG_BWD", "set_debug", "debug_enabled", "workspace_error", "stream_ceiling", "release_capture_workspaces",
 ]
 
@@ -97,6 +97,7 @@ def load_library(path: str):
                                           p]),
         "linear_attention_workspace_bytes": (sz, [p, i32]),
         "linear_attention_fwd": (i32, [p, i32, p, p, p, p, p, p, p, p, sz, p]),
+        "linear_attention_bwd": (i32, [p, i32, p, p, p, p, p, p, p, p, p, p, p, i32, p, p, sz, p]),
         "linear_attention_step": (i32, [p, i32, p, p, p, p, p, ctypes.c_int32, p, p, p]),
         "qk_norm_rope_fwd": (i32, [p, i32, p, p, p, p, p, p, p]),
         "qk_norm_rope_workspace_bytes": (sz, [p]),
@@ -604,8 +605,8 @@ def matrix_affine_scan_bwd(A, h, dy, h0=None, cu_seqlens=None, reverse=False, ne
 # ---------------------------------------------------------------------------
 # linear attention (see _attention.py)
 # ---------------------------------------------------------------------------
-from ._attention import (linear_attention_fwd, linear_attention_step, qk_norm_rope_bwd,  # noqa: E402
-                         qk_norm_rope_fwd)
+from ._attention import (linear_attention_bwd, linear_attention_fwd, linear_attention_step,  # noqa: E402
+                         qk_norm_rope_bwd, qk_norm_rope_fwd)
 
 
 # ---------------------------------------------------------------------------

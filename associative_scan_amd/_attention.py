@@ -1,6 +1,7 @@
 """Python binding of the linear attention operators (see include/mscan.h).
 
     linear_attention_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=None, need_ht=True) -> (o, ht)
+    linear_attention_bwd(q, k, v, g, do, h0=None, dht=None, ...) -> (dq, dk, dv, dg, dh0)
     linear_attention_step(q, k, v, g, state, slots=None, scale=None) -> o        (state updated in place)
     qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions=None, eps=1e-6, interleaved=False) -> (q', k')
     qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, dq', dk', ...) -> (dq, dk, dq_weight, dk_weight)
@@ -144,6 +145,35 @@ def linear_attention_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=None, need_
             ctypes.byref(prob), dt, ctypes.byref(qh), ctypes.byref(kh), ctypes.byref(vh), _ptr(g), _ptr(h0), _ptr(o),
             _ptr(ht), _ptr(ws), n, _stream_handle(dev)))
     return o, ht
+
+
+def linear_attention_bwd(q, k, v, g, do, h0=None, dht=None, cu_seqlens=None, scale=None, need_dg=True, need_dh0=True):
+    """Adjoint of linear_attention_fwd for the gradients do of o and dht of ht
+    (None: zero): (dq, dk, dv, dg, dh0), dg of g's shape and dh0 in fp32 (None
+    when not needed)."""
+    prob, dt, cu, nseg = _attention(q, k, v, g, cu_seqlens, scale)
+    dev = q.device
+    shape = (nseg, prob.H, prob.Dk, prob.Dv)
+    h0, dht = _states(h0, shape, "h0", dev), _states(dht, shape, "dht", dev)
+    if do.shape != v.shape or do.dtype != v.dtype or do.device != dev:
+        raise ValueError("do must have the shape, dtype and device of v")
+    qh, kh, vh, oh = _heads(q, "q"), _heads(k, "k"), _heads(v, "v"), _heads(do, "do")
+    dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k, v))
+    dg = torch.empty(g.shape, dtype=torch.float32, device=dev) if need_dg else None
+    dh0 = torch.empty(shape, dtype=torch.float32, device=dev) if need_dh0 else None
+    if prob.B == 0 or prob.T == 0 or nseg == 0:
+        if need_dg:
+            dg.zero_()
+        if need_dh0:
+            dh0.zero_() if dht is None else dh0.copy_(dht)
+        return dq, dk, dv, dg, dh0
+    with _on(dev):
+        ws, n = _space(prob, 1, dev)
+        _check("linear_attention_bwd", lib.linear_attention_bwd(
+            ctypes.byref(prob), dt, ctypes.byref(qh), ctypes.byref(kh), ctypes.byref(vh), _ptr(g), ctypes.byref(oh),
+            _ptr(h0), _ptr(dht), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), int(g.dim() == 1), _ptr(dh0), _ptr(ws), n,
+            _stream_handle(dev)))
+    return dq, dk, dv, dg, dh0
 
 
 def linear_attention_step(q, k, v, g, state, slots=None, scale=None):

@@ -81,6 +81,30 @@ FwdSpace fwd_space(const LaProblem& r) {
   return w;
 }
 
+// Offsets of the backward's workspace.
+struct BwdSpace {
+  size_t states = 0, lams = 0, totals = 0, dq_part = 0, dk_part = 0, rows = 0, dg_part = 0, bytes = 0;
+};
+BwdSpace bwd_space(const LaProblem& r) {
+  BwdSpace w;
+  const size_t tokens = (size_t)r.B * r.T, cells = (size_t)r.slots * r.H * r.Dk * r.Dv * 4;
+  auto take = [&](size_t n) {
+    const size_t at = w.bytes;
+    w.bytes += up256(n);
+    return at;
+  };
+  const bool split = r.T > r.span;
+  w.states = take(split ? cells : 0);
+  w.lams = take(split ? cells : 0);
+  w.totals = take(split ? (size_t)r.slots * r.H * 4 : 0);
+  const size_t part = r.H != r.Hk ? tokens * r.H * r.Dk * 4 : 0;
+  w.dq_part = take(part);
+  w.dk_part = take(part);
+  w.rows = take((2 * tokens * r.H + (size_t)r.slots * r.H) * 4);
+  w.dg_part = take((size_t)r.slots * r.H * 8);
+  return w;
+}
+
 mscan_status check_norm(const mscan_norm_rope* p, int dtype) {
   if (!p) return MSCAN_ERR_INVALID;
   if (dtype != MSCAN_F32 && dtype != MSCAN_BF16 && dtype != MSCAN_F16) return MSCAN_ERR_UNSUPPORTED;
@@ -124,7 +148,7 @@ size_t linear_attention_workspace_bytes(const mscan_attention* prob, int backwar
   if (check(prob) != MSCAN_OK || backward < 0 || backward > 1) return 0;
   const LaProblem r = problem(prob, nullptr, backward == 1);
   if (check_blocks(r) != MSCAN_OK) return 0;
-  return fwd_space(r).bytes + 256;
+  return (backward ? bwd_space(r).bytes : fwd_space(r).bytes) + 256;
 }
 
 mscan_status linear_attention_fwd(const mscan_attention* prob, int dtype, const mscan_heads* q, const mscan_heads* k,
@@ -150,6 +174,45 @@ mscan_status linear_attention_fwd(const mscan_attention* prob, int dtype, const 
   a.states = w.bytes ? (float*)((char*)ws + w.states) : nullptr;
   a.totals = w.bytes ? (float*)((char*)ws + w.totals) : nullptr;
   return hip_status(mscan::la::launch_fwd(a, dtype, (hipStream_t)stream));
+}
+
+mscan_status linear_attention_bwd(const mscan_attention* prob, int dtype, const mscan_heads* q, const mscan_heads* k,
+                                  const mscan_heads* v, const float* g, const mscan_heads* dO, const float* h0,
+                                  const float* dht, void* dq, void* dk, void* dv, float* dg, int dg_per_head,
+                                  float* dh0, void* ws, size_t ws_bytes, void* stream) {
+  mscan_status s = check(prob);
+  if (s != MSCAN_OK) return s;
+  if (dtype != MSCAN_F32 && dtype != MSCAN_BF16 && dtype != MSCAN_F16) return MSCAN_ERR_UNSUPPORTED;
+  mscan::la::BwdArgs a{};
+  a.pr = problem(prob, g, true);
+  const int share = prob->H / prob->Hk;
+  if ((s = heads(q, dtype, share, prob->Dk, a.q)) != MSCAN_OK) return s;
+  if ((s = heads(k, dtype, share, prob->Dk, a.k)) != MSCAN_OK) return s;
+  if ((s = heads(v, dtype, 1, prob->Dv, a.v)) != MSCAN_OK) return s;
+  if ((s = heads(dO, dtype, 1, prob->Dv, a.dO)) != MSCAN_OK) return s;
+  if (!g || ((uintptr_t)g & 3u) || ((uintptr_t)dg & 3u)) return MSCAN_ERR_INVALID;
+  if (!dq || !dk || !dv || !aligned16(dq) || !aligned16(dk) || !aligned16(dv)) return MSCAN_ERR_INVALID;
+  if (!aligned16(h0) || !aligned16(dht) || !aligned16(dh0)) return MSCAN_ERR_INVALID;
+  if ((s = check_blocks(a.pr)) != MSCAN_OK) return s;
+  const BwdSpace w = bwd_space(a.pr);
+  if (!ws || !aligned16(ws) || ws_bytes < w.bytes) return MSCAN_ERR_WORKSPACE;
+  char* base = (char*)ws;
+  a.h0 = h0;
+  a.dht = dht;
+  a.dq = dq;
+  a.dk = dk;
+  a.dv = dv;
+  a.dg = dg;
+  a.dg_sum = dg_per_head != 0;
+  a.dh0 = dh0;
+  a.states = (float*)(base + w.states);
+  a.lams = (float*)(base + w.lams);
+  a.totals = (float*)(base + w.totals);
+  a.dq_part = share > 1 ? (float*)(base + w.dq_part) : nullptr;
+  a.dk_part = share > 1 ? (float*)(base + w.dk_part) : nullptr;
+  a.rows = (float*)(base + w.rows);
+  a.dg_part = (double*)(base + w.dg_part);
+  return hip_status(mscan::la::launch_bwd(a, dtype, (hipStream_t)stream));
 }
 
 mscan_status linear_attention_step(const mscan_attention* prob, int dtype, const mscan_heads* q, const mscan_heads* k,

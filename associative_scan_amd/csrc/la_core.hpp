@@ -220,6 +220,54 @@ __device__ __forceinline__ void store_state(const f16v (&S)[DX / 32], float* p, 
       }
 }
 
+// The same for ldx = 1: the wave's view is the transpose of the memory's rows.
+template <int DX>
+__device__ __forceinline__ void load_state_t(f16v (&S)[DX / 32], const float* p, int ldz, int dx, int dz, int z0) {
+  const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 2;
+  const int n = p && z < dz ? dx : 0;
+  p += r0 + (int64_t)z * ldz;
+#pragma unroll
+  for (int t = 0; t < DX / 32; ++t)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      f4v v = {0.f, 0.f, 0.f, 0.f};
+      if (t * 32 + a * 8 < n) v = *(const f4v*)(p + t * 32 + a * 8);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) S[t][a * 4 + i] = v[i];
+    }
+}
+
+template <int CTRL>
+__device__ __forceinline__ float ror_add(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, false));
+}
+__device__ __forceinline__ float sum16(float x) {  // over the 16 lanes of a DPP row, to all of them
+  return ror_add<0x121>(ror_add<0x122>(ror_add<0x124>(ror_add<0x128>(x))));
+}
+// Sums over the wave's 32 columns of acc times the rows of a tile, to dst[C].
+template <class TM, int C, int D>
+__device__ __forceinline__ void row_dots(const f16v (&acc)[C / 32], const TM* tile, int z0, float* dst) {
+  const int l = fresh_lane(), z = z0 + (l & 31), h4 = (l >> 5) << 2;
+  constexpr int N = C / 4;  // values of a lane, halved by the exchange between DPP rows
+  float w[C / 2];
+#pragma unroll
+  for (int i = 0; i < C / 2; ++i) {
+    const int row = (i >> 4) * 32 + (((i & 15) >> 2) << 3) + h4 + (i & 3);
+    w[i] = acc[i >> 4][i & 15] * (float)tile[unit_at<TM, D>(row, z >> 2) + (z & 3)];
+  }
+  float mine = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    // the first DPP row of a pair sums value i, the second value i + N
+    const auto x = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, w[i]),
+                                                    __builtin_bit_cast(uint32_t, w[i + N]), false, false);
+    const float v = sum16(__builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]));
+    mine = (l & 15) == i ? v : mine;
+  }
+  const int i = (l & 15) + ((l >> 4) & 1) * N;
+  if ((l & 15) < N) dst[(i >> 4) * 32 + (((i & 15) >> 2) << 3) + h4 + (i & 3)] = mine;
+}
+
 // Rows of an output, [n][H][d] from out (stride st), the wave's 32 columns.
 template <class TOut, int C>
 __device__ __forceinline__ void store_rows(const f16v (&acc)[C / 32], TOut* out, int64_t st, int n, int d, int z0) {

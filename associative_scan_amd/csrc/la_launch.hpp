@@ -32,6 +32,13 @@ struct LaProblem {
 // Steps per span, for LaProblem::span; sets spans and slots too.
 void plan(LaProblem& p, bool backward);
 
+// The states between spans: what each span adds (see k_span_states), and from
+// these the states at the spans' starts (rev: the adjoint's at their ends).
+hipError_t launch_span_states(const LaProblem& p, int dtype, bool rev, const Heads& y, const Heads& z, float sz,
+                              float* states, float* totals, hipStream_t st);
+hipError_t launch_join(const LaProblem& p, bool rev, const float* outer, float* states, const float* totals,
+                       hipStream_t st);
+
 struct FwdArgs {
   LaProblem pr;
   Heads q, k, v;
@@ -69,8 +76,8 @@ struct BwdArgs {
   float *states, *totals;   // as in FwdArgs (split problems)
   float *lams;              // split problems: the adjoint state after each span
   float *dq_part, *dk_part; // shared heads: [B][T][H][Dk] each
-  float *rows;              // dg: [2][B][T][H], and one value per (slot, head) behind it
-  float *dg_part;           // dg_sum: [B][T][H]
+  float* rows;              // dg: [2][B][T][H], and one value per (slot, head) behind them
+  double* dg_part;          // dg_sum: [slots][H]
 };
 hipError_t launch_bwd(const BwdArgs& a, int dtype, hipStream_t st);
 

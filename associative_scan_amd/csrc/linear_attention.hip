@@ -144,15 +144,36 @@ void plan(LaProblem& p, bool backward) {
 }
 
 template <class TIn, class TM, int DX, int NW>
+static hipError_t states_dims(const LaProblem& p, bool rev, const Heads& y, const Heads& z, float sz, float* states,
+                              float* totals, hipStream_t st) {
+  const unsigned blocks = (unsigned)((int64_t)p.slots * p.H);
+  if (rev)
+    hipLaunchKernelGGL((k_span_states<TIn, TM, DX, NW, true>), dim3(blocks), dim3(NW * 64), 0, st, p, y, z, sz, states,
+                       totals);
+  else
+    hipLaunchKernelGGL((k_span_states<TIn, TM, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, p, y, z, sz,
+                       states, totals);
+  return hipGetLastError();
+}
+template <class TIn, class TM>
+static hipError_t states_type(const LaProblem& p, bool rev, const Heads& y, const Heads& z, float sz, float* states,
+                              float* totals, hipStream_t st) {
+  if (p.Dk <= 64)
+    return p.Dv <= 64 ? states_dims<TIn, TM, 64, 2>(p, rev, y, z, sz, states, totals, st)
+                      : states_dims<TIn, TM, 64, 4>(p, rev, y, z, sz, states, totals, st);
+  return p.Dv <= 64 ? states_dims<TIn, TM, 128, 2>(p, rev, y, z, sz, states, totals, st)
+                    : states_dims<TIn, TM, 128, 4>(p, rev, y, z, sz, states, totals, st);
+}
+hipError_t launch_span_states(const LaProblem& p, int dtype, bool rev, const Heads& y, const Heads& z, float sz,
+                              float* states, float* totals, hipStream_t st) {
+  if (dtype == 0) return states_type<float, float>(p, rev, y, z, sz, states, totals, st);
+  if (dtype == 1) return states_type<__bf16, __bf16>(p, rev, y, z, sz, states, totals, st);
+  return states_type<_Float16, float>(p, rev, y, z, sz, states, totals, st);
+}
+
+template <class TIn, class TM, int DX, int NW>
 static hipError_t fwd_dims(const FwdArgs& a, hipStream_t st) {
   const unsigned blocks = (unsigned)((int64_t)a.pr.slots * a.pr.H);
-  if (a.pr.T > a.pr.span) {
-    hipLaunchKernelGGL((k_span_states<TIn, TM, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, a.pr, a.k, a.v,
-                       1.f, a.states, a.totals);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-    if ((e = launch_join(a.pr, false, a.h0, a.states, a.totals, st)) != hipSuccess) return e;
-  }
   hipLaunchKernelGGL((k_attn_fwd<TIn, TM, DX, NW>), dim3(blocks), dim3(NW * 64), 0, st, a);
   return hipGetLastError();
 }
@@ -167,6 +188,11 @@ static hipError_t fwd_type(const FwdArgs& a, hipStream_t st) {
 }
 
 hipError_t launch_fwd(const FwdArgs& a, int dtype, hipStream_t st) {
+  if (a.pr.T > a.pr.span) {
+    hipError_t e = launch_span_states(a.pr, dtype, false, a.k, a.v, 1.f, a.states, a.totals, st);
+    if (e != hipSuccess) return e;
+    if ((e = launch_join(a.pr, false, a.h0, a.states, a.totals, st)) != hipSuccess) return e;
+  }
   if (dtype == 0) return fwd_type<float, float>(a, st);
   if (dtype == 1) return fwd_type<__bf16, __bf16>(a, st);
   return fwd_type<_Float16, float>(a, st);

@@ -1,0 +1,392 @@
+// Linear attention, backward.
+//
+// dq runs forward in time like the forward pass, with (do, v, k) in the places
+// of (q, k, v) and the state's transpose; dk and dv run backward in time with
+// the adjoint state Lam_t = scale q_t do_t^T + e^{g_{t+1}} Lam_{t+1}, in one
+// kernel: half of its waves hold Lam for dv = (k, q, do), the other half its
+// transpose for dk = (v, do, q), on the same four tiles in LDS.
+//
+// The gradient of a decay, dg_t = e^{g_t} <Lam_t, S_{t-1}>, is the sum over
+// i >= t > j of W_ij = scale e^{..} (q_i . k_j) (do_i . v_j), so that
+// dg_t = dg_{t+1} + q_t . dq_t - k_t . dk_t. The kernels give each step's
+// q . dq - k . dk in fp32 (without the i = j terms, which cancel), and every
+// span starts from its own <Lam, S> at its end, so a sum runs over one span.
+#include "la_core.hpp"
+
+namespace mscan {
+namespace la {
+
+// Sum over a workgroup of up to 8 waves; the result is thread 0's.
+__device__ __forceinline__ float block_sum(float x, float* lds) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) x += __shfl_xor(x, m);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = x;
+  __syncthreads();
+  float s = 0.f;
+  for (unsigned w = 0; w < blockDim.x / 64; ++w) s += lds[w];
+  return s;
+}
+
+// DX: columns of do and v; NW waves of 32 columns of k and dq.
+template <class TIn, class TM, int DX, int NW, bool DG>
+__global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
+  constexpr int C = kChunk<TM>, DZ = NW * 32, NT = NW * 64, NP = kPiecesP<TM>;
+  constexpr int kScratch = NP * C * C > C * DZ ? NP * C * C : C * DZ;
+  __shared__ __align__(16) TM O[C * DX];
+  __shared__ __align__(16) TM V[C * DX];
+  __shared__ __align__(16) TM K[C * DZ];
+  __shared__ __align__(16) TM P[kScratch];  // q until the row sums are done, then the scores
+  __shared__ __align__(16) Decays<C> dec;
+  __shared__ float part[NW][C];
+  const LaProblem& pr = a.pr;
+  const int tid = threadIdx.x, wave = tid >> 6, z0 = wave * 32;
+  const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
+  const Span sp = find_span(pr, slot);
+  const int64_t row0 = (sp.batch * pr.T + sp.t0) * pr.H + h;  // of [B][T][H] arrays
+  const bool shared = a.dq_part != nullptr;
+  const int64_t ost = (int64_t)pr.H * pr.Dk;
+  float* rows = a.rows;
+  if (pr.cu && sp.seq >= pr.nseg) {  // steps behind the last sequence
+    for (int64_t i = tid; i < (int64_t)sp.n * pr.Dk; i += NT) {
+      const int64_t at = row0 * pr.Dk + i / pr.Dk * ost + i % pr.Dk;
+      if (shared) a.dq_part[at] = 0.f;
+      else ((TIn*)a.dq)[at] = (TIn)0.f;
+    }
+    return;
+  }
+  if (sp.n == 0) return;
+  const int64_t cells = (int64_t)pr.Dk * pr.Dv, state = ((int64_t)slot * pr.H + h) * cells;
+  const int64_t outer = ((int64_t)sp.seq * pr.H + h) * cells;
+  f16v S[DX / 32];
+  load_state_t<DX>(S, sp.is_first ? (a.h0 ? a.h0 + outer : nullptr) : a.states + state, pr.Dv, pr.Dv, pr.Dk, z0);
+  const TIn* op = head_base<TIn>(a.dO, sp.batch, sp.t0, h);
+  const TIn* vp = head_base<TIn>(a.v, sp.batch, sp.t0, h);
+  const TIn* kp = head_base<TIn>(a.k, sp.batch, sp.t0, h);
+  const TIn* qp = head_base<TIn>(a.q, sp.batch, sp.t0, h);
+  const float* gp = gate_base(pr, sp.batch, sp.t0, h);
+  TileRegs<TIn, C, DX, NT> ro, rv;
+  TileRegs<TIn, C, DZ, NT> rk, rq;
+  float rg = 0.f;
+  auto fetch = [&](int t) {
+    ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t, tid);
+    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t, tid);
+    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t, tid);
+    if constexpr (DG) rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t, tid);
+    if (wave == 0) rg = load_gate(gp, pr.gst, t, sp.n);
+  };
+  fetch(0);
+  for (int t = 0; t < sp.n; t += C) {
+    ro.store(O, tid);
+    rv.store(V, tid);
+    rk.store(K, tid);
+    if constexpr (DG) rq.store(P, tid);
+    if (wave == 0) write_decays<C>(dec, rg);
+    __syncthreads();
+    if (t + C < sp.n) fetch(t + C);
+    f16v acc[C / 32];
+    from_state<TM, C, DX, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(O, S, acc);
+    scale_rows<C>(acc, dec.up, pr.scale);
+    if constexpr (DG) {
+      row_dots<TM, C, DZ>(acc, P, z0, part[wave]);
+      __syncthreads();
+      if (tid < C && t + tid < sp.n) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) s += part[w][tid];
+        rows[row0 + (int64_t)(t + tid) * pr.H] = s;
+      }
+    }
+    scores<TM, C, DX, NP, false>(O, V, P, dec, pr.scale, wave, NW);
+    __syncthreads();
+    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(V, K, P, dec, 1.f, z0, S, acc);
+    const int64_t at = row0 * pr.Dk + (int64_t)t * ost;
+    if (shared) store_rows<float, C>(acc, a.dq_part + at, ost, sp.n - t, pr.Dk, z0);
+    else store_rows<TIn, C>(acc, (TIn*)a.dq + at, ost, sp.n - t, pr.Dk, z0);
+    __syncthreads();
+  }
+  if constexpr (DG) {  // <Lam, S> at the end of the span
+    const float* lam = sp.is_last ? (a.dht ? a.dht + outer : nullptr) : a.lams + state;
+    float s = 0.f;
+    if (lam) {
+      f16v L[DX / 32];
+      load_state_t<DX>(L, lam, pr.Dv, pr.Dv, pr.Dk, z0);
+#pragma unroll
+      for (int i = 0; i < DX / 32; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) s += L[i][r] * S[i][r];
+    }
+    s = block_sum(s, &part[0][0]);
+    if (tid == 0) rows[2 * pr.B * pr.T * pr.H + (int64_t)slot * pr.H + h] = s;
+  }
+}
+
+// dk and dv. D: columns of every tile; NW waves for dv, then NW for dk.
+template <class TIn, class TM, int D, bool DG>
+__global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
+  constexpr int C = kChunk<TM>, NW = D / 32, NT = NW * 128, NP = kPiecesP<TM>;
+  __shared__ __align__(16) TM Q[C * D];
+  __shared__ __align__(16) TM K[C * D];
+  __shared__ __align__(16) TM V[C * D];
+  __shared__ __align__(16) TM O[C * D];
+  __shared__ __align__(16) TM P[2][NP * C * C];
+  __shared__ __align__(16) Decays<C> dec;
+  __shared__ float part[NW][C];
+  __shared__ float sums[kTiles<C>][2][16];
+  const LaProblem& pr = a.pr;
+  const int tid = threadIdx.x, wave = tid >> 6;
+  const bool is_dk = wave >= NW;
+  const int z0 = (is_dk ? wave - NW : wave) * 32;
+  const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
+  const Span sp = find_span(pr, slot);
+  const int64_t row0 = (sp.batch * pr.T + sp.t0) * pr.H + h;
+  const bool shared = a.dk_part != nullptr;
+  const int64_t kst = (int64_t)pr.H * pr.Dk, vst = (int64_t)pr.H * pr.Dv;
+  float* rows = a.rows + pr.B * pr.T * pr.H;
+  if (pr.cu && sp.seq >= pr.nseg) {
+    for (int64_t i = tid; i < (int64_t)sp.n * pr.Dk; i += NT) {
+      const int64_t at = row0 * pr.Dk + i / pr.Dk * kst + i % pr.Dk;
+      if (shared) a.dk_part[at] = 0.f;
+      else ((TIn*)a.dk)[at] = (TIn)0.f;
+    }
+    for (int64_t i = tid; i < (int64_t)sp.n * pr.Dv; i += NT)
+      ((TIn*)a.dv)[row0 * pr.Dv + i / pr.Dv * vst + i % pr.Dv] = (TIn)0.f;
+    return;
+  }
+  if (sp.n == 0 && !sp.is_first) return;
+  const int64_t cells = (int64_t)pr.Dk * pr.Dv, state = ((int64_t)slot * pr.H + h) * cells;
+  const int64_t outer = ((int64_t)sp.seq * pr.H + h) * cells;
+  const float* lam = sp.is_last ? (a.dht ? a.dht + outer : nullptr) : a.lams + state;
+  f16v S[NW];
+  if (is_dk) load_state_t<D>(S, lam, pr.Dv, pr.Dv, pr.Dk, z0);
+  else load_state<D>(S, lam, pr.Dv, 1, pr.Dk, pr.Dv, z0);
+  const TM* X = is_dk ? V : K;
+  const TM* Y = is_dk ? O : Q;
+  const TM* Z = is_dk ? Q : O;
+  const TIn* qp = head_base<TIn>(a.q, sp.batch, sp.t0, h);
+  const TIn* kp = head_base<TIn>(a.k, sp.batch, sp.t0, h);
+  const TIn* vp = head_base<TIn>(a.v, sp.batch, sp.t0, h);
+  const TIn* op = head_base<TIn>(a.dO, sp.batch, sp.t0, h);
+  const float* gp = gate_base(pr, sp.batch, sp.t0, h);
+  TileRegs<TIn, C, D, NT> rq, rk, rv, ro;
+  float rg = 0.f;
+  auto fetch = [&](int t) {
+    rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t, tid);
+    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t, tid);
+    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t, tid);
+    ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t, tid);
+    if (wave == 0) rg = load_gate(gp, pr.gst, t, sp.n);
+  };
+  const int last = sp.n > 0 ? (sp.n - 1) / C * C : -C;
+  if (last >= 0) fetch(last);
+  for (int t = last; t >= 0; t -= C) {
+    rq.store(Q, tid);
+    rk.store(K, tid);
+    rv.store(V, tid);
+    ro.store(O, tid);
+    if (wave == 0) write_decays<C>(dec, rg);
+    __syncthreads();
+    if (t > 0) fetch(t - C);
+    {  // scores of both roles, and W's sums over i and over j
+      const int l = fresh_lane();
+      for (int i = wave; i < kTiles<C>; i += 2 * NW) {
+        int rt, ct;
+        tile_of<C, true>(i, rt, ct);
+        const f4v d = decay_tile<C, true>(dec, rt, ct, l);
+        f4v x = score_tile<TM, D>(K, Q, rt, ct, l);
+        f4v y = score_tile<TM, D>(V, O, rt, ct, l);
+        float row[4], col = 0.f;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float f = d[e] * pr.scale;
+          x[e] = d[e] != 0.f ? x[e] * f : 0.f;
+          const bool strict = ct * 16 + ((l >> 4) << 2) + e > rt * 16 + (l & 15);
+          row[e] = strict ? x[e] * y[e] : 0.f;
+          col += row[e];
+          y[e] = d[e] != 0.f ? y[e] * f : 0.f;
+        }
+        put_tile<TM, C, NP>(P[0], x, rt, ct, l);
+        put_tile<TM, C, NP>(P[1], y, rt, ct, l);
+        if constexpr (DG) {
+          col += __shfl_xor(col, 16);
+          col += __shfl_xor(col, 32);
+          if (l < 16) sums[i][0][l] = col;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            row[e] = sum16(row[e]);
+            if ((l & 15) == e) sums[i][1][((l >> 4) << 2) + e] = row[e];
+          }
+        }
+      }
+    }
+    f16v acc[C / 32];
+    from_state<TM, C, D, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(X, S, acc);
+    scale_rows<C>(acc, dec.dn, 1.f);
+    if constexpr (DG)
+      if (is_dk) row_dots<TM, C, D>(acc, K, z0, part[wave - NW]);
+    __syncthreads();
+    if constexpr (DG)
+      if (tid < C && t + tid < sp.n) {
+        float s = 0.f;
+#pragma unroll
+        for (int w = 0; w < NW; ++w) s -= part[w][tid];
+#pragma unroll
+        for (int i = 0; i < kTiles<C>; ++i) {
+          int rt, ct;
+          tile_of<C, true>(i, rt, ct);
+          if (ct == tid >> 4) s += sums[i][1][tid & 15];
+          if (rt == tid >> 4) s -= sums[i][0][tid & 15];
+        }
+        rows[row0 + (int64_t)(t + tid) * pr.H] = s;
+      }
+    within_chunk<TM, C, D, D, NP, kPiecesZ<TM>, true>(Y, Z, P[is_dk], dec, pr.scale, z0, S, acc);
+    if (is_dk) {
+      const int64_t at = row0 * pr.Dk + (int64_t)t * kst;
+      if (shared) store_rows<float, C>(acc, a.dk_part + at, kst, sp.n - t, pr.Dk, z0);
+      else store_rows<TIn, C>(acc, (TIn*)a.dk + at, kst, sp.n - t, pr.Dk, z0);
+    } else {
+      store_rows<TIn, C>(acc, (TIn*)a.dv + row0 * pr.Dv + (int64_t)t * vst, vst, sp.n - t, pr.Dv, z0);
+    }
+    __syncthreads();
+  }
+  if (sp.is_first && a.dh0 && !is_dk) store_state<D>(S, a.dh0 + outer, pr.Dv, 1, pr.Dk, pr.Dv, z0);
+}
+
+// Gradients of shared heads: the sum over the heads that read one, in order.
+template <class TIn>
+__global__ __launch_bounds__(256) void k_sum_heads(const float* part, void* out, int64_t n, int share, int d) {
+  // n: groups of 4 elements of [tokens][Hk][d]
+  for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += (int64_t)gridDim.x * 256) {
+    const int64_t e = i * 4, head = e / d, c = e - head * d;
+    const float* p = part + head * share * d + c;
+    f4v s = {0.f, 0.f, 0.f, 0.f};
+    for (int r = 0; r < share; ++r) s += *(const f4v*)(p + (int64_t)r * d);
+    TIn* o = (TIn*)out + e;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) o[j] = (TIn)s[j];
+  }
+}
+
+// dg: sums from a span's end to each of its steps, 8 heads by 32 parts of the
+// span on a workgroup, in fp64. SUM: their total over the span instead.
+template <bool SUM>
+__global__ __launch_bounds__(256) void k_gate_grad(const LaProblem pr, const float* rows, float* dg, double* total) {
+  __shared__ double sums[32][8];
+  const int nh = (pr.H + 7) / 8;
+  const int slot = blockIdx.x / nh, h = (blockIdx.x % nh) * 8 + (int)(threadIdx.x & 7), p = threadIdx.x >> 3;
+  const Span sp = find_span(pr, slot);
+  const bool behind = pr.cu && sp.seq >= pr.nseg;
+  const int64_t n = pr.B * pr.T * pr.H, row0 = (sp.batch * pr.T + sp.t0) * pr.H + h;
+  const int len = (sp.n + 31) / 32, first = p * len;
+  int end = first + len < sp.n ? first + len : sp.n;
+  if (h >= pr.H) end = first;
+  if (behind) {
+    if constexpr (!SUM)
+      for (int t = first; t < end; ++t) dg[row0 + (int64_t)t * pr.H] = 0.f;
+    if (SUM && p == 0 && h < pr.H) total[(int64_t)slot * pr.H + h] = 0.0;
+    return;
+  }
+  const float* A = rows + row0;
+  const float* R = rows + n + row0;
+  double s = 0.0;
+#pragma unroll 4
+  for (int t = first; t < end; ++t) s += (double)A[(int64_t)t * pr.H] + (double)R[(int64_t)t * pr.H];
+  sums[p][threadIdx.x & 7] = s;
+  __syncthreads();
+  if (h >= pr.H) {
+    if (!SUM) return;
+  }
+  double v = h < pr.H && sp.n > 0 ? (double)rows[2 * n + (int64_t)slot * pr.H + h] : 0.0;
+  for (int i = p + 1; i < 32; ++i) v += sums[i][threadIdx.x & 7];
+  double all = 0.0;
+#pragma unroll 4
+  for (int t = end - 1; t >= first; --t) {
+    v += (double)A[(int64_t)t * pr.H] + (double)R[(int64_t)t * pr.H];
+    if constexpr (SUM) all += v;
+    else dg[row0 + (int64_t)t * pr.H] = (float)v;
+  }
+  if constexpr (SUM) {
+    __syncthreads();
+    sums[p][threadIdx.x & 7] = all;
+    __syncthreads();
+    if (p == 0 && h < pr.H) {
+      double x = 0.0;
+      for (int i = 0; i < 32; ++i) x += sums[i][threadIdx.x & 7];
+      total[(int64_t)slot * pr.H + h] = x;
+    }
+  }
+}
+__global__ __launch_bounds__(256) void k_gate_total(const double* total, int slots, int H, float* dg) {
+  __shared__ double sums[256];
+  const int h = blockIdx.x;
+  double s = 0.0;
+  for (int i = threadIdx.x; i < slots; i += 256) s += total[(int64_t)i * H + h];
+  sums[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    double x = 0.0;
+    for (int i = 0; i < 256; ++i) x += sums[i];
+    dg[h] = (float)x;
+  }
+}
+
+template <class TIn, class TM, int DX, int NW>
+static hipError_t dq_dims(const BwdArgs& a, hipStream_t st) {
+  const unsigned blocks = (unsigned)((int64_t)a.pr.slots * a.pr.H);
+  if (a.dg) hipLaunchKernelGGL((k_attn_dq<TIn, TM, DX, NW, true>), dim3(blocks), dim3(NW * 64), 0, st, a);
+  else hipLaunchKernelGGL((k_attn_dq<TIn, TM, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, a);
+  return hipGetLastError();
+}
+template <class TIn, class TM, int D>
+static hipError_t dkv_dims(const BwdArgs& a, hipStream_t st) {
+  const unsigned blocks = (unsigned)((int64_t)a.pr.slots * a.pr.H);
+  if (a.dg) hipLaunchKernelGGL((k_attn_dkv<TIn, TM, D, true>), dim3(blocks), dim3(D * 4), 0, st, a);
+  else hipLaunchKernelGGL((k_attn_dkv<TIn, TM, D, false>), dim3(blocks), dim3(D * 4), 0, st, a);
+  return hipGetLastError();
+}
+
+template <class TIn, class TM>
+static hipError_t bwd_type(const BwdArgs& a, int dtype, hipStream_t st) {
+  const LaProblem& pr = a.pr;
+  hipError_t e;
+  if (pr.T > pr.span) {
+    if ((e = launch_span_states(pr, dtype, false, a.k, a.v, 1.f, a.states, a.totals, st)) != hipSuccess) return e;
+    if ((e = launch_join(pr, false, a.h0, a.states, a.totals, st)) != hipSuccess) return e;
+    if ((e = launch_span_states(pr, dtype, true, a.q, a.dO, pr.scale, a.lams, a.totals, st)) != hipSuccess) return e;
+    if ((e = launch_join(pr, true, a.dht, a.lams, a.totals, st)) != hipSuccess) return e;
+  }
+  const bool k64 = pr.Dk <= 64, v64 = pr.Dv <= 64;
+  e = v64 ? (k64 ? dq_dims<TIn, TM, 64, 2>(a, st) : dq_dims<TIn, TM, 64, 4>(a, st))
+          : (k64 ? dq_dims<TIn, TM, 128, 2>(a, st) : dq_dims<TIn, TM, 128, 4>(a, st));
+  if (e != hipSuccess) return e;
+  e = k64 && v64 ? dkv_dims<TIn, TM, 64>(a, st) : dkv_dims<TIn, TM, 128>(a, st);
+  if (e != hipSuccess) return e;
+  if (a.dq_part) {
+    const int64_t n = pr.B * pr.T * pr.Hk * pr.Dk / 4, want = (n + 255) / 256;
+    const unsigned blocks = (unsigned)(want < 4096 ? want : 4096);
+    const int share = pr.H / pr.Hk;
+    hipLaunchKernelGGL((k_sum_heads<TIn>), dim3(blocks), dim3(256), 0, st, a.dq_part, a.dq, n, share, pr.Dk);
+    hipLaunchKernelGGL((k_sum_heads<TIn>), dim3(blocks), dim3(256), 0, st, a.dk_part, a.dk, n, share, pr.Dk);
+    if ((e = hipGetLastError()) != hipSuccess) return e;
+  }
+  if (a.dg) {
+    const unsigned blocks = (unsigned)((int64_t)pr.slots * ((pr.H + 7) / 8));
+    if (a.dg_sum) {
+      hipLaunchKernelGGL((k_gate_grad<true>), dim3(blocks), dim3(256), 0, st, pr, a.rows, a.dg, a.dg_part);
+      hipLaunchKernelGGL(k_gate_total, dim3(pr.H), dim3(256), 0, st, a.dg_part, pr.slots, pr.H, a.dg);
+    } else {
+      hipLaunchKernelGGL((k_gate_grad<false>), dim3(blocks), dim3(256), 0, st, pr, a.rows, a.dg, a.dg_part);
+    }
+    e = hipGetLastError();
+  }
+  return e;
+}
+
+hipError_t launch_bwd(const BwdArgs& a, int dtype, hipStream_t st) {
+  if (dtype == 0) return bwd_type<float, float>(a, dtype, st);
+  if (dtype == 1) return bwd_type<__bf16, __bf16>(a, dtype, st);
+  return bwd_type<_Float16, float>(a, dtype, st);
+}
+
+}  // namespace la
+}  // namespace mscan

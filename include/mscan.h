@@ -290,6 +290,20 @@ MSCAN_API mscan_status linear_attention_fwd(const mscan_attention* prob, int dty
                                             const float* h0, void* o, float* ht, void* ws, size_t ws_bytes,
                                             void* stream);
 
+/* Backward: gradients for do (dtype, strided [B][T][H][Dv]) and dht (or NULL:
+ * zero), from the forward's inputs alone. With Lam_t = scale q_t do_t^T +
+ * e^{g_{t+1}} Lam_{t+1} (Lam past the end of a sequence = dht):
+ *   dq_t = scale S_t do_t, dk_t = Lam_t v_t, dv_t = Lam_t^T k_t,
+ *   dg_t = e^{g_t} <Lam_t, S_{t-1}>, dh0 = e^{g_1} Lam_1.
+ * dq, dk of shared heads are sums over the heads that read them.
+ *   dg : fp32 [B][T][H], or [H], its sum over all steps, when dg_per_head; or
+ *        NULL. dh0 : or NULL; an empty sequence has dh0 = dht.              */
+MSCAN_API mscan_status linear_attention_bwd(const mscan_attention* prob, int dtype, const mscan_heads* q,
+                                            const mscan_heads* k, const mscan_heads* v, const float* g,
+                                            const mscan_heads* dO, const float* h0, const float* dht, void* dq,
+                                            void* dk, void* dv, float* dg, int dg_per_head, float* dh0, void* ws,
+                                            size_t ws_bytes, void* stream);
+
 /* One step of prob->B sequences (T = 1, nseg = B, cu_seqlens NULL) against a
  * pool of states, [pool][H][Dk][Dv] fp32, updated in place:
  *   S = e^{g_b} S + k_b v_b^T, o_b = scale S^T q_b, S = state[slots[b]].

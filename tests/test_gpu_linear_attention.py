@@ -193,3 +193,138 @@ def test_empty_shapes(m):
     assert o.shape == (2, 0, 3, 16) and torch.equal(ht, h0)
     o, ht = m.linear_attention_fwd(z(0, 5, 3, 8), z(0, 5, 3, 8), z(0, 5, 3, 16), torch.zeros(3, device=DEV))
     assert o.shape == (0, 5, 3, 16) and ht.shape == (0, 3, 8, 16)
+
+
+# ---------------------------------------------------------------------------
+# backward. dg is a sum of differences q . dq - k . dk over the steps up to a
+# span's end (at most 1024 here): beside its own magnitude it carries their
+# rounding, (T + Dk + Dv + 256) 2^-24 of each one's magnitude. These are
+# independent, so their sum is held to the root of their number times the largest.
+# ---------------------------------------------------------------------------
+def check_backward(m, x, cu=None, scale=None, h0=True, dht=True, dtype="bf16"):
+    q, k, v, g, s0, do, dh = x
+    s0, dh = s0 if h0 else None, dh if dht else None
+    c = None if cu is None else torch.tensor(cu, dtype=torch.int32, device=DEV)
+    got = m.linear_attention_bwd(q, k, v, g, do, h0=s0, dht=dh, cu_seqlens=c, scale=scale)
+    sc = q.shape[3] ** -0.5 if scale is None else scale
+    want = ref.backward(f64(q), f64(k), f64(v), f64(g), f64(do), f64(s0), f64(dh), cu, sc)
+    T, Dk, Dv = q.shape[1], q.shape[3], v.shape[3]
+    for n, a, w in zip(("dq", "dk", "dv", "dg", "dh0"), got, want):
+        if n == "dg":
+            val, mag = w
+            rows = (np.abs(f64(q)) * want[0][1]).sum(3) + (np.abs(f64(k)) * want[1][1]).sum(3)
+            r = v.shape[2] // q.shape[2]
+            mag = mag + min(T, 1024) ** 0.5 * np.repeat(rows, r, 2).max(1, keepdims=True)
+            if g.dim() == 1:
+                val, mag = val.sum((0, 1)), mag.sum((0, 1))
+            w = (val, mag)
+        close(a, w, n, T, Dk, Dv, dtype)
+    return got
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("T", [1, 2, 31, 33, 64, 65, 130, 256, 257, 600])
+def test_backward_lengths(m, T, dtype):
+    check_backward(m, make(T, 2, T, 3, 64, 64, dtype), dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("Dk,Dv", [(8, 8), (16, 40), (40, 16), (64, 128), (128, 64), (72, 96), (96, 72), (128, 128),
+                                   (120, 104), (8, 128), (128, 8)])
+def test_backward_head_sizes(m, Dk, Dv, dtype):
+    check_backward(m, make(Dk + Dv, 1, 300, 2, Dk, Dv, dtype), dtype=dtype)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_backward_shared_heads_and_head_decays(m, dtype):
+    check_backward(m, make(1, 2, 150, 6, 64, 32, dtype, Hk=2), dtype=dtype)
+    check_backward(m, make(2, 1, 700, 4, 128, 64, dtype, Hk=1, gate="head"), dtype=dtype, h0=False, scale=0.5)
+    check_backward(m, make(3, 3, 100, 11, 16, 16, dtype, gate="head"), dtype=dtype, dht=False)
+
+
+@pytest.mark.parametrize("cu", CUTS, ids=str)
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_backward_packed(m, cu, dtype):
+    check_backward(m, make(len(cu), 1, 300, 2, 64, 64, dtype, n=len(cu) - 1), cu=cu, dtype=dtype)
+    check_backward(m, make(len(cu), 1, 300, 2, 64, 64, dtype, n=len(cu) - 1), cu=cu, dtype=dtype, h0=False, dht=False)
+
+
+def test_backward_packed_many_spans(m):
+    cu = [0, 900, 900, 901, 1300, 2600, 2601]
+    check_backward(m, make(5, 1, 2601, 2, 128, 128, n=6, spread=(3.0, 9.0)), cu=cu)
+    check_backward(m, make(5, 1, 2601, 4, 64, 64, Hk=1, n=6, gate="head"), cu=cu)
+
+
+def test_backward_spans(m):
+    check_backward(m, make(6, 2, 1500, 2, 128, 128, spread=(4.0, 12.0)))
+    check_backward(m, make(7, 1, 1025, 1, 64, 64, "fp32", spread=(8.0, 8.0)), dtype="fp32")
+
+
+def test_backward_resets(m):
+    x = make(8, 1, 200, 2, 64, 64)
+    g = x[3]
+    g[:, 0] = -float("inf")
+    g[:, 63:66] = -float("inf")
+    g[:, 100] = -1e30
+    g[:, 101] = -200.0
+    dg = check_backward(m, x)[3]
+    g[:] = -float("inf")
+    assert torch.isfinite(dg).all() and torch.isfinite(check_backward(m, x)[3]).all()
+
+
+def test_backward_nan_stays_in_its_sequence(m):
+    cu = [0, 70, 150, 300]
+    q, k, v, g, h0, do, dht = make(9, 1, 300, 2, 64, 64, n=3)
+    c = torch.tensor(cu, dtype=torch.int32, device=DEV)
+    want = m.linear_attention_bwd(q, k, v, g, do, h0=h0, dht=dht, cu_seqlens=c)
+    for bad in (float("nan"), float("inf")):
+        y = [t.clone() for t in (q, k, v, g, do)]
+        for t in y:
+            t[:, 75:149] = bad
+        h2, d2 = h0.clone(), dht.clone()
+        h2[1], d2[1] = bad, bad
+        got = m.linear_attention_bwd(*y, h0=h2, dht=d2, cu_seqlens=c)
+        for a, w in zip(got[:4], want[:4]):
+            assert torch.equal(a[:, :70], w[:, :70]) and torch.equal(a[:, 150:], w[:, 150:])
+        assert torch.equal(got[4][0], want[4][0]) and torch.equal(got[4][2], want[4][2])
+
+
+@pytest.mark.parametrize("Hk", [2, 1])
+def test_backward_steps_behind_the_last_sequence(m, Hk):
+    q, k, v, g, h0, do, dht = make(10, 1, 700, 2, 64, 64, n=2, Hk=Hk)
+    do[:, 310:] = float("nan")
+    c = torch.tensor([0, 300, 310], dtype=torch.int32, device=DEV)
+    got = m.linear_attention_bwd(q, k, v, g, do, h0=h0, dht=dht, cu_seqlens=c)
+    cut = lambda t: t[:, :310]  # noqa: E731
+    want = m.linear_attention_bwd(cut(q), cut(k), cut(v), cut(g), cut(do), h0=h0, dht=dht, cu_seqlens=c)
+    for a, w in zip(got[:4], want[:4]):
+        assert torch.equal(a[:, 310:], torch.zeros_like(a[:, 310:]))
+        assert torch.equal(a[:, :310], w)
+    assert torch.equal(got[4], want[4])
+    d1 = m.linear_attention_bwd(q, k, v, g[0, 0].contiguous(), do, h0=h0, dht=dht, cu_seqlens=c)[3]
+    assert torch.isfinite(d1).all()
+
+
+def test_backward_parts_and_repeats(m):
+    q, k, v, g, h0, do, dht = make(12, 2, 2100, 3, 128, 128)
+    want = m.linear_attention_bwd(q, k, v, g, do, h0=h0, dht=dht)
+    for _ in range(3):
+        for a, b in zip(want, m.linear_attention_bwd(q, k, v, g, do, h0=h0, dht=dht)):
+            assert torch.equal(a, b)
+    dq, dk, dv, dg, dh0 = m.linear_attention_bwd(q, k, v, g, do, h0=h0, dht=dht, need_dg=False, need_dh0=False)
+    assert dg is None and dh0 is None
+    for a, b in zip((dq, dk, dv), want):
+        # without dg the state enters a product as two pieces instead of three
+        assert (a.float() - b.float()).norm() <= 2 ** -8 * b.float().norm()
+
+
+def test_backward_strides(m):
+    q, k, v, g, h0, do, dht = make(11, 2, 140, 4, 64, 32)
+    want = m.linear_attention_bwd(q, k, v, g, do, h0=h0, dht=dht)
+    hm = lambda x: x.transpose(1, 2).contiguous().transpose(1, 2)  # noqa: E731
+    for a, b in zip(want, m.linear_attention_bwd(hm(q), hm(k), hm(v), hm(g), hm(do), h0=h0, dht=dht)):
+        assert torch.equal(a, b)
+    # the gradient of a sum: one broadcast row of do
+    ones = torch.ones(1, 1, 1, 32, device=DEV, dtype=q.dtype).expand(2, 140, 4, 32)
+    for a, b in zip(m.linear_attention_bwd(q, k, v, g, ones), m.linear_attention_bwd(q, k, v, g, ones.contiguous())):
+        assert torch.equal(a, b)
