@@ -25,14 +25,31 @@ constexpr int kPiecesXExact = sizeof(TM) == 2 ? 3 : 1;
 
 __device__ __forceinline__ int acc_row(int r) { return ((r >> 2) << 3) + ((lane_id() >> 5) << 2) + (r & 3); }
 
+// A lane's offsets into the tiles (see la_device.hpp).
+template <class TM, int C, int DX, int DZ>
+struct LaneOffsets {
+  int x32, x16, y, z, p;
+  __device__ __forceinline__ explicit LaneOffsets(int z0)
+      : x32(row_lane<TM, DX, 32>()), x16(row_lane<TM, DX, 16>()), y(col_lane<TM, DX, true>()),
+        z(moved<TM, DZ>(col_lane<TM, DZ, false>(), 0, z0 / kUnit<TM>)), p(row_lane<TM, C, 32>()) {}
+};
+
 // One 16 x 16 tile of the scores x_r . y_c, transposed: rows ct*16 + 4 (l / 16)
 // + i, i < 4, are steps c, column rt*16 + (l & 15) is step r.
 template <class TM, int DX>
-__device__ __forceinline__ f4v score_tile(const TM* X, const TM* Y, int rt, int ct, int l) {
+__device__ __forceinline__ f4v score_tile(const TM* X, const TM* Y, int x16, int rt, int ct) {
+  const TM* x = X + rt * 16 * DX;  // 16 rows leave the units' order as it is
+  const TM* y = Y + ct * 16 * DX;
+  typename Math<TM>::Frag xf[DX / 32], yf[DX / 32];
+#pragma unroll
+  for (int i = 0; i < DX / 32; ++i) {
+    yf[i] = row_frag<TM, DX>(y, x16, 0, i * 32);
+    xf[i] = row_frag<TM, DX>(x, x16, 0, i * 32);
+  }
+  step_fence();
   f4v acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int k0 = 0; k0 < DX; k0 += 32)
-    acc = Math<TM>::mma16(row_frag16<TM, DX>(Y, ct * 16, k0, l), row_frag16<TM, DX>(X, rt * 16, k0, l), acc);
+  for (int i = 0; i < DX / 32; ++i) acc = Math<TM>::mma16(yf[i], xf[i], acc);
   return acc;
 }
 // The decays of such a tile: e^{b_r - b_c} for c <= r (REV: e^{b_c - b_r} for
@@ -54,11 +71,11 @@ __device__ __forceinline__ f4v decay_tile(const Decays<C>& d, int rt, int ct, in
 // Masked scores into P [NP][C][C] (row r, column c).
 template <class TM, int C, int NP>
 __device__ __forceinline__ void put_tile(TM* P, f4v val, int rt, int ct, int l) {
-  const int r = rt * 16 + (l & 15), u = ct * 4 + (l >> 4);
-  typename Math<TM>::Unit piece[NP];
+  const int off = cell_at<TM, C>(rt * 16 + (l & 15), ct * 16 + ((l >> 4) << 2));
+  typename Four<TM>::type piece[NP];
   split4<TM, NP>(val, piece);
 #pragma unroll
-  for (int p = 0; p < NP; ++p) *(typename Math<TM>::Unit*)(P + p * C * C + unit_at<TM, C>(r, u)) = piece[p];
+  for (int p = 0; p < NP; ++p) *(typename Four<TM>::type*)(P + p * C * C + off) = piece[p];
 }
 // The 16 x 16 tiles that a product over P reads: for every 32 rows, the columns
 // up to their end (REV: from their start). Tile i of kTiles<C>.
@@ -81,14 +98,14 @@ __device__ __forceinline__ void tile_of(int i, int& rt, int& ct) {
   }
 }
 template <class TM, int C, int DX, int NP, bool REV>
-__device__ __forceinline__ void scores(const TM* X, const TM* Y, TM* P, const Decays<C>& d, float scale, int wave,
-                                       int nwaves) {
+__device__ __forceinline__ void scores(const TM* X, const TM* Y, int x16, TM* P, const Decays<C>& d, float scale,
+                                       int wave, int nwaves) {
   const int l = fresh_lane();
   for (int i = wave; i < kTiles<C>; i += nwaves) {
     int rt, ct;
     tile_of<C, REV>(i, rt, ct);
     const f4v dec = decay_tile<C, REV>(d, rt, ct, l);
-    f4v acc = score_tile<TM, DX>(X, Y, rt, ct, l);
+    f4v acc = score_tile<TM, DX>(X, Y, x16, rt, ct);
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = dec[e] != 0.f ? acc[e] * (dec[e] * scale) : 0.f;
     put_tile<TM, C, NP>(P, acc, rt, ct, l);
@@ -104,30 +121,49 @@ __device__ __forceinline__ f8v state8(const f16v (&S)[NT], int s) {
                  : __builtin_shufflevector(t, t, 0, 1, 2, 3, 4, 5, 6, 7);
 }
 
-// acc[rt] = rows of X times the state
+// Orders a step's instructions as one matrix product and then N others, over and
+// over: a wave that issues its products back to back waits for each of them with
+// the vector ALU idle.
+template <int PRODUCTS, int N>
+__device__ __forceinline__ void interleave() {
+#pragma unroll
+  for (int i = 0; i < PRODUCTS; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x8, 1, 0);  // matrix
+    __builtin_amdgcn_sched_group_barrier(0x2, N, 0);  // vector ALU
+  }
+}
+
+// acc[rt] = rows of X times the state. A step issues the reads of the next one
+// and splits the next one's state between its own products.
 template <class TM, int C, int DX, int NS>
-__device__ __forceinline__ void from_state(const TM* X, const f16v (&S)[DX / 32], f16v (&acc)[C / 32]) {
+__device__ __forceinline__ void from_state(const TM* X, int x32, const f16v (&S)[DX / 32], f16v (&acc)[C / 32]) {
 #pragma unroll
   for (int rt = 0; rt < C / 32; ++rt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[rt][r] = 0.f;
-  const int l = fresh_lane();
+  typename Math<TM>::Frag x[2][C / 32], piece[2][NS];
+#pragma unroll
+  for (int rt = 0; rt < C / 32; ++rt) x[0][rt] = row_frag<TM, DX>(X, x32, rt * 32, 0);
+  split8<TM, NS>(state8<DX / 32>(S, 0), piece[0]);
 #pragma unroll
   for (int s = 0; s < DX / 16; ++s) {
     step_fence();
-    typename Math<TM>::Frag piece[NS];
-    split8<TM, NS>(state8<DX / 32>(S, s), piece);
+    if (s + 1 < DX / 16) {
 #pragma unroll
-    for (int rt = 0; rt < C / 32; ++rt) {
-      const typename Math<TM>::Frag x = row_frag32<TM, DX>(X, rt * 32, s * 16, l);
-#pragma unroll
-      for (int p = 0; p < NS; ++p) acc[rt] = Math<TM>::mma32(x, piece[p], acc[rt]);
+      for (int rt = 0; rt < C / 32; ++rt) x[(s + 1) & 1][rt] = row_frag<TM, DX>(X, x32, rt * 32, (s + 1) * 16);
     }
+    step_fence();
+#pragma unroll
+    for (int p = 0; p < NS; ++p)
+#pragma unroll
+      for (int rt = 0; rt < C / 32; ++rt) acc[rt] = Math<TM>::mma32(x[s & 1][rt], piece[s & 1][p], acc[rt]);
+    if (s + 1 < DX / 16) split8<TM, NS>(state8<DX / 32>(S, s + 1), piece[(s + 1) & 1]);
+    if constexpr (sizeof(TM) == 2) interleave<NS * (C / 32), 7>();
   }
 }
-// rows of acc times f[row] * s
+// rows of acc times f[row]
 template <int C>
-__device__ __forceinline__ void scale_rows(f16v (&acc)[C / 32], const float* f, float s) {
+__device__ __forceinline__ void scale_rows(f16v (&acc)[C / 32], const float* f) {
   const int h4 = (fresh_lane() >> 5) << 2;
 #pragma unroll
   for (int rt = 0; rt < C / 32; ++rt)
@@ -135,7 +171,7 @@ __device__ __forceinline__ void scale_rows(f16v (&acc)[C / 32], const float* f, 
     for (int a = 0; a < 4; ++a) {
       const f4v w = *(const f4v*)(f + rt * 32 + a * 8 + h4);
 #pragma unroll
-      for (int i = 0; i < 4; ++i) acc[rt][a * 4 + i] *= w[i] * s;
+      for (int i = 0; i < 4; ++i) acc[rt][a * 4 + i] *= w[i];
     }
 }
 template <int NT>
@@ -145,93 +181,109 @@ __device__ __forceinline__ void scale_state(f16v (&S)[NT], float f) {
 #pragma unroll
     for (int r = 0; r < 16; ++r) S[t][r] *= f;
 }
-// S += Y^T (f z) for one 16-step js; z: the wave's 32 columns of those steps
-template <class TM, int DX, int NS>
-__device__ __forceinline__ void into_state(const TM* Y, typename Math<TM>::Frag z, const float* f, float s, int js,
-                                           int l, f16v (&S)[DX / 32]) {
-  const int h = l >> 5;
-  const f4v fa = *(const f4v*)(f + js * 16 + 4 * h), fb = *(const f4v*)(f + js * 16 + 8 + 4 * h);
+// The wave's 32 columns of Z for one 16-step js, times f, in pieces.
+template <class TM, int NS>
+__device__ __forceinline__ void weigh(typename Math<TM>::Frag z, const float* f, int js,
+                                      typename Math<TM>::Frag (&piece)[NS]) {
+  const int h = lane_id() >> 5;
+  const f4v fa = *(const f4v*)(f + js * 16 + 8 * h), fb = *(const f4v*)(f + js * 16 + 8 * h + 4);
   f8v w = Math<TM>::widen(z);
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    w[i] *= fa[i] * s;
-    w[4 + i] *= fb[i] * s;
+    w[i] *= fa[i];
+    w[4 + i] *= fb[i];
   }
-  typename Math<TM>::Frag piece[NS];
   split8<TM, NS>(w, piece);
-#pragma unroll
-  for (int t = 0; t < DX / 32; ++t) {
-    const typename Math<TM>::Frag y = col_frag32<TM, DX>(Y, js * 16, t * 32, l);
-#pragma unroll
-    for (int p = 0; p < NS; ++p) S[t] = Math<TM>::mma32(y, piece[p], S[t]);
-  }
 }
-// acc += P Z, and S = e^{b_C} S + Y^T (f Z), sharing the reads of Z
+// S = e^{b_C} S + Y^T (in Z) and, with P, acc += P Z on the same reads of Z.
 template <class TM, int C, int DX, int DZ, int NP, int NS, bool REV>
-__device__ __forceinline__ void within_chunk(const TM* Y, const TM* Z, const TM* P, const Decays<C>& d, float sz,
-                                             int z0, f16v (&S)[DX / 32], f16v (&acc)[C / 32]) {
+__device__ __forceinline__ void within_chunk(const TM* Y, const TM* Z, const TM* P, const Decays<C>& d,
+                                             const LaneOffsets<TM, C, DX, DZ>& at, f16v (&S)[DX / 32],
+                                             f16v (&acc)[C / 32]) {
+  typedef typename Math<TM>::Frag Frag;
+  constexpr int RT = C / 32, KP = NP > 0 ? NP : 1, JS = C / 16;
+  Frag z[2], y[DX / 32], pf[RT][KP], piece[2][NS];
+  const auto inside = [](int rt, int js) { return REV ? js * 16 >= rt * 32 : js * 16 < rt * 32 + 32; };
+  z[0] = col_frag<TM, DZ>(Z, at.z, 0, 0);
+  if (JS > 1) z[1] = col_frag<TM, DZ>(Z, at.z, 16, 0);
   scale_state<DX / 32>(S, d.all);
-  const int l = fresh_lane();
+  weigh<TM, NS>(z[0], d.in, 0, piece[0]);
 #pragma unroll
-  for (int js = 0; js < C / 16; ++js) {
+  for (int js = 0; js < JS; ++js) {
     step_fence();
-    const typename Math<TM>::Frag z = col_frag32<TM, DZ>(Z, js * 16, z0, l);
 #pragma unroll
-    for (int rt = 0; rt < C / 32; ++rt) {
-      if (REV ? js * 16 < rt * 32 : js * 16 >= rt * 32 + 32) continue;
+    for (int rt = 0; rt < RT; ++rt)
+      if (inside(rt, js))
 #pragma unroll
-      for (int p = 0; p < NP; ++p)
-        acc[rt] = Math<TM>::mma32(row_frag32<TM, C>(P + p * C * C, rt * 32, js * 16, l), z, acc[rt]);
-    }
-    into_state<TM, DX, NS>(Y, z, REV ? d.up : d.dn, sz, js, l, S);
+        for (int p = 0; p < NP; ++p) pf[rt][p] = row_frag<TM, C>(P + p * C * C, at.p, rt * 32, js * 16);
+#pragma unroll
+    for (int t = 0; t < DX / 32; ++t) y[t] = col_frag<TM, DX>(Y, at.y, js * 16, t * 32);
+    step_fence();
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        if (inside(rt, js)) acc[rt] = Math<TM>::mma32(pf[rt][p], z[js & 1], acc[rt]);
+#pragma unroll
+    for (int p = 0; p < NS; ++p)
+#pragma unroll
+      for (int t = 0; t < DX / 32; ++t) S[t] = Math<TM>::mma32(y[t], piece[js & 1][p], S[t]);
+    if (js + 1 < JS) weigh<TM, NS>(z[(js + 1) & 1], d.in, js + 1, piece[(js + 1) & 1]);
+    if (js + 2 < JS) z[js & 1] = col_frag<TM, DZ>(Z, at.z, (js + 2) * 16, 0);
+    if constexpr (sizeof(TM) == 2) interleave<NS * (DX / 32) + NP, 5>();
   }
 }
 
 // The wave's 32 columns of a state in memory: element (x, z) of the wave's
-// view is at x * ldx + z * ldz, x < dx, z < dz (dx, dz multiples of 8).
+// view is at x * ldx + z * ldz, x < dx, z < dz (dx, dz multiples of 8). Register
+// 4 a + i of tile t is entry t*32 + (a / 2) 16 + 8 h + (a % 2) 4 + i.
 template <int DX>
 __device__ __forceinline__ void load_state(f16v (&S)[DX / 32], const float* p, int ldx, int ldz, int dx, int dz,
                                            int z0) {
-  const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 2;
-  const int n = p && z < dz ? dx : 0;
+  const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 3;
+  const int n = p && z < dz ? dx - r0 : 0;
   p += (int64_t)r0 * ldx + (int64_t)z * ldz;
 #pragma unroll
   for (int t = 0; t < DX / 32; ++t)
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      const bool in = t * 32 + a * 8 < n;
+      const int x = t * 32 + (a >> 1) * 16 + (a & 1) * 4;
+      const bool in = x < n;
 #pragma unroll
-      for (int i = 0; i < 4; ++i) S[t][a * 4 + i] = in ? p[(int64_t)(t * 32 + a * 8 + i) * ldx] : 0.f;
+      for (int i = 0; i < 4; ++i) S[t][a * 4 + i] = in ? p[(int64_t)(x + i) * ldx] : 0.f;
     }
 }
 template <int DX>
 __device__ __forceinline__ void store_state(const f16v (&S)[DX / 32], float* p, int ldx, int ldz, int dx, int dz,
                                             int z0) {
-  const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 2;
-  const int n = z < dz ? dx : 0;
+  const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 3;
+  const int n = z < dz ? dx - r0 : 0;
   p += (int64_t)r0 * ldx + (int64_t)z * ldz;
 #pragma unroll
   for (int t = 0; t < DX / 32; ++t)
 #pragma unroll
-    for (int a = 0; a < 4; ++a)
-      if (t * 32 + a * 8 < n) {
+    for (int a = 0; a < 4; ++a) {
+      const int x = t * 32 + (a >> 1) * 16 + (a & 1) * 4;
+      if (x < n) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) p[(int64_t)(t * 32 + a * 8 + i) * ldx] = S[t][a * 4 + i];
+        for (int i = 0; i < 4; ++i) p[(int64_t)(x + i) * ldx] = S[t][a * 4 + i];
       }
+    }
 }
 
 // The same for ldx = 1: the wave's view is the transpose of the memory's rows.
 template <int DX>
 __device__ __forceinline__ void load_state_t(f16v (&S)[DX / 32], const float* p, int ldz, int dx, int dz, int z0) {
-  const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 2;
-  const int n = p && z < dz ? dx : 0;
+  const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 3;
+  const int n = p && z < dz ? dx - r0 : 0;
   p += r0 + (int64_t)z * ldz;
 #pragma unroll
   for (int t = 0; t < DX / 32; ++t)
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
+      const int x = t * 32 + (a >> 1) * 16 + (a & 1) * 4;
       f4v v = {0.f, 0.f, 0.f, 0.f};
-      if (t * 32 + a * 8 < n) v = *(const f4v*)(p + t * 32 + a * 8);
+      if (x < n) v = *(const f4v*)(p + x);
 #pragma unroll
       for (int i = 0; i < 4; ++i) S[t][a * 4 + i] = v[i];
     }
@@ -247,13 +299,13 @@ __device__ __forceinline__ float sum16(float x) {  // over the 16 lanes of a DPP
 // Sums over the wave's 32 columns of acc times the rows of a tile, to dst[C].
 template <class TM, int C, int D>
 __device__ __forceinline__ void row_dots(const f16v (&acc)[C / 32], const TM* tile, int z0, float* dst) {
-  const int l = fresh_lane(), z = z0 + (l & 31), h4 = (l >> 5) << 2;
+  const int l = fresh_lane(), h4 = (l >> 5) << 2, off = cell_at<TM, D>(h4, z0 + (l & 31));
   constexpr int N = C / 4;  // values of a lane, halved by the exchange between DPP rows
   float w[C / 2];
 #pragma unroll
   for (int i = 0; i < C / 2; ++i) {
-    const int row = (i >> 4) * 32 + (((i & 15) >> 2) << 3) + h4 + (i & 3);
-    w[i] = acc[i >> 4][i & 15] * (float)tile[unit_at<TM, D>(row, z >> 2) + (z & 3)];
+    const int row = (i >> 4) * 32 + (((i & 15) >> 2) << 3) + (i & 3);
+    w[i] = acc[i >> 4][i & 15] * (float)tile[moved<TM, D>(off, row, 0)];
   }
   float mine = 0.f;
 #pragma unroll
@@ -268,7 +320,48 @@ __device__ __forceinline__ void row_dots(const f16v (&acc)[C / 32], const TM* ti
   if ((l & 15) < N) dst[(i >> 4) * 32 + (((i & 15) >> 2) << 3) + h4 + (i & 3)] = mine;
 }
 
-// Rows of an output, [n][H][d] from out (stride st), the wave's 32 columns.
+// Rows of an output: the wave's 32 columns of acc as TOut into a [C][D] array in
+// LDS, from there as whole 16-byte units to registers, and to [n][..][d] in
+// memory. A thread takes the units that TileRegs::store writes, so the next
+// chunk's tile of that shape can take the same place without a barrier. The
+// stores to memory come after the next tiles' waits for their loads, which would
+// otherwise wait for the stores too.
+template <class TOut, int C, int D>
+__device__ __forceinline__ void rows_to_lds(const f16v (&acc)[C / 32], TOut* tile, int z0) {
+  const int l = fresh_lane(), off = cell_at<TOut, D>((l >> 5) << 2, z0 + (l & 31));
+#pragma unroll
+  for (int rt = 0; rt < C / 32; ++rt)
+#pragma unroll
+    for (int r = 0; r < 16; ++r)
+      tile[moved<TOut, D>(off, rt * 32 + ((r >> 2) << 3) + (r & 3), 0)] = (TOut)acc[rt][r];
+}
+template <class TOut, int C, int D, int NT>
+struct OutRegs {
+  static constexpr int STEP = NT / (D / 8), N = C / STEP, W = sizeof(TOut) == 4 ? 2 : 1;
+  u4v r[N][W];
+  __device__ __forceinline__ void take(const TOut* tile) {
+    const int tid = fresh_thread();
+    const int off = unit_at<TOut, D>(tid / (D / 8), (tid % (D / 8)) * (8 / kUnit<TOut>));
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+      for (int w = 0; w < W; ++w) r[i][w] = *(const u4v*)(tile + moved<TOut, D>(off, i * STEP, w));
+  }
+  __device__ __forceinline__ void put(TOut* out, int64_t st, int n, int d) const {
+    const int tid = fresh_thread(), row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
+    TOut* p = out + row0 * st + c;
+    if (c >= d) n = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      if (row0 + i * STEP < n) {
+#pragma unroll
+        for (int w = 0; w < W; ++w) *(u4v*)(p + w * 4) = r[i][w];
+      }
+      p += STEP * st;
+    }
+  }
+};
+// The same straight from registers, two rows of 32 columns at a time.
 template <class TOut, int C>
 __device__ __forceinline__ void store_rows(const f16v (&acc)[C / 32], TOut* out, int64_t st, int n, int d, int z0) {
   const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 2;
@@ -323,31 +416,33 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
 #pragma unroll
     for (int r = 0; r < 16; ++r) S[t][r] = 0.f;
   const int nc = (sp.n + C - 1) / C;
-  TileRegs<TIn, C, DX, NT> ry;
-  TileRegs<TIn, C, DZ, NT> rz;
-  float rg = 0.f;
+  // loads run two chunks ahead: a chunk's own work is shorter than a load
+  TileRegs<TIn, C, DX, NT> ry[2];
+  TileRegs<TIn, C, DZ, NT> rz[2];
+  float rg[2] = {0.f, 0.f};
   double total = 0.0;
-  auto fetch = [&](int i) {
+  const LaneOffsets<TM, C, DX, DZ> at(z0);
+  f16v none[C / 32];
+  const auto fetch = [&](int i, int s) {
     const int c = REV ? nc - 1 - i : i, t = c * C;
-    ry.load(yp + (int64_t)t * y.st, y.st, y.d, sp.n - t, tid);
-    rz.load(zp + (int64_t)t * z.st, z.st, z.d, sp.n - t, tid);
-    if (wave == 0) rg = load_gate(gp, pr.gst, t, sp.n);
+    ry[s].load(yp + (int64_t)t * y.st, y.st, y.d, sp.n - t);
+    rz[s].load(zp + (int64_t)t * z.st, z.st, z.d, sp.n - t);
+    if (wave == 0) rg[s] = load_gate(gp, pr.gst, t, sp.n);
   };
-  fetch(0);
-  for (int i = 0; i < nc; ++i) {
-    ry.store(Y, tid);
-    rz.store(Z, tid);
-    if (wave == 0) total += write_decays<C>(dec, rg);
+  const auto chunk = [&](int i, int s) {
+    ry[s].store(Y);
+    rz[s].store(Z);
+    if (wave == 0) total += write_decays<C, REV>(dec, rg[s], sz);
     __syncthreads();
-    if (i + 1 < nc) fetch(i + 1);
-    scale_state<DX / 32>(S, dec.all);
-    const int l = fresh_lane();
-#pragma unroll
-    for (int js = 0; js < C / 16; ++js) {
-      step_fence();
-      into_state<TM, DX, kPiecesZ<TM>>(Y, col_frag32<TM, DZ>(Z, js * 16, z0, l), REV ? dec.up : dec.dn, sz, js, l, S);
-    }
+    if (i + 2 < nc) fetch(i + 2, s);
+    within_chunk<TM, C, DX, DZ, 0, kPiecesZ<TM>, REV>(Y, Z, nullptr, dec, at, S, none);
     __syncthreads();
+  };
+  fetch(0, 0);
+  if (nc > 1) fetch(1, 1);
+  for (int i = 0; i < nc; i += 2) {
+    chunk(i, 0);
+    if (i + 1 < nc) chunk(i + 1, 1);
   }
   store_state<DX>(S, states + ((int64_t)slot * pr.H + h) * pr.Dk * pr.Dv, pr.Dv, 1, pr.Dk, pr.Dv, z0);
   if (tid == 0) totals[(int64_t)slot * pr.H + h] = exp2_fast((float)total);

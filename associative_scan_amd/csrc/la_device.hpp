@@ -42,6 +42,11 @@ __device__ __forceinline__ int fresh_lane() {
   asm volatile("" : "+v"(l));
   return l;
 }
+__device__ __forceinline__ int fresh_thread() {
+  int t = (int)threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
 // Keeps the reads of later steps of a phase from being moved ahead, which
 // would hold their results in registers too.
 __device__ __forceinline__ void step_fence() { __builtin_amdgcn_sched_barrier(0); }
@@ -49,13 +54,13 @@ __device__ __forceinline__ void step_fence() { __builtin_amdgcn_sched_barrier(0)
 // ---------------------------------------------------------------------------
 // matrix-core fragments
 //
-// A fragment holds 8 values per lane of an operand's contraction axis. Lanes l
-// and l + 32 (32-wide tiles) take the axis entries {4h + j, 8 + 4h + j}, j < 4,
-// h = l / 32, of a 16-step: the entries that an accumulator of the previous
-// product holds in 8 consecutive registers, so a state kept in accumulators is
-// an operand without a move between lanes. Both operands use the same order, so
-// the product does not depend on it. fp32 math issues eight products of one
-// value per lane in place of one 16-bit product of eight.
+// A fragment holds 8 values per lane of an operand's contraction axis: lanes l
+// and l + 32 of a 32-wide tile take entries 8 h .. 8 h + 7, h = l / 32, of a
+// 16-step. An accumulator of a state holds, in 8 consecutive registers, rows
+// 8 e + 4 h + i (e < 2, i < 4) of 16; the state's rows are numbered so that these
+// are its entries 8 h + 4 e + i (state_row), which makes a state kept in
+// accumulators an operand without a move between lanes. fp32 math issues eight
+// products of one value per lane in place of one 16-bit product of eight.
 // ---------------------------------------------------------------------------
 template <class TM>
 struct Math;
@@ -63,15 +68,11 @@ struct Math;
 template <>
 struct Math<__bf16> {
   typedef bf8 Frag;
-  typedef bf4 Unit;  // 4 consecutive elements of a tile row
   static __device__ __forceinline__ f16v mma32(Frag a, Frag b, f16v c) {
     return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
   }
   static __device__ __forceinline__ f4v mma16(Frag a, Frag b, f4v c) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ Frag join(Unit a, Unit b) {
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   }
   static __device__ __forceinline__ f8v widen(Frag f) { return __builtin_convertvector(f, f8v); }
 };
@@ -79,7 +80,6 @@ struct Math<__bf16> {
 template <>
 struct Math<float> {
   typedef f8v Frag;
-  typedef f4v Unit;
   static __device__ __forceinline__ f16v mma32(Frag a, Frag b, f16v c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
@@ -90,104 +90,154 @@ struct Math<float> {
     for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
     return c;
   }
-  static __device__ __forceinline__ Frag join(Unit a, Unit b) {
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
   static __device__ __forceinline__ f8v widen(Frag f) { return f; }
 };
 
+// Two fp32 values rounded to bf16 in one register. As an instruction of its own:
+// the compiler otherwise converts a value twice, once for the pair and once for
+// what the rounding leaves.
+__device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
+  uint32_t w;
+  asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(w) : "v"(a), "v"(b));
+  return w;
+}
 // x as a sum of N fragments: bf16 pieces of 8 bits each, every piece the
 // rounding of what the ones before it left (N = 2: off by 2^-18 of x at most,
 // N = 3: exact but for fp32's own last bits); fp32 math takes x whole.
+template <int N, int E>
+__device__ __forceinline__ void split_pairs(float (&x)[E], uint32_t (&out)[N][E / 2]) {
+#pragma unroll
+  for (int p = 0; p < N; ++p)
+#pragma unroll
+    for (int i = 0; i < E; i += 2) {
+      const uint32_t w = bf16_pair(x[i], x[i + 1]);
+      out[p][i / 2] = w;
+      if (p + 1 < N) {
+        x[i] -= __builtin_bit_cast(float, w << 16);
+        x[i + 1] -= __builtin_bit_cast(float, w & 0xffff0000u);
+      }
+    }
+}
 template <class TM, int N>
 __device__ __forceinline__ void split8(f8v x, typename Math<TM>::Frag (&out)[N]) {
   if constexpr (sizeof(TM) == 4) {
     out[0] = x;
   } else {
+    float v[8];
+    uint32_t w[N][4];
 #pragma unroll
-    for (int p = 0; p < N; ++p) {
-      out[p] = __builtin_convertvector(x, bf8);
-      if (p + 1 < N) x -= __builtin_convertvector(out[p], f8v);
-    }
+    for (int i = 0; i < 8; ++i) v[i] = x[i];
+    split_pairs<N, 8>(v, w);
+#pragma unroll
+    for (int p = 0; p < N; ++p) out[p] = __builtin_bit_cast(bf8, u4v{w[p][0], w[p][1], w[p][2], w[p][3]});
   }
 }
+template <class TM>
+struct Four;  // 4 consecutive elements of a tile row
+template <>
+struct Four<__bf16> {
+  typedef u2v type;
+};
+template <>
+struct Four<float> {
+  typedef f4v type;
+};
 template <class TM, int N>
-__device__ __forceinline__ void split4(f4v x, typename Math<TM>::Unit (&out)[N]) {
+__device__ __forceinline__ void split4(f4v x, typename Four<TM>::type (&out)[N]) {
   if constexpr (sizeof(TM) == 4) {
     out[0] = x;
   } else {
+    float v[4] = {x[0], x[1], x[2], x[3]};
+    uint32_t w[N][2];
+    split_pairs<N, 4>(v, w);
 #pragma unroll
-    for (int p = 0; p < N; ++p) {
-      out[p] = __builtin_convertvector(x, bf4);
-      if (p + 1 < N) x -= __builtin_convertvector(out[p], f4v);
-    }
+    for (int p = 0; p < N; ++p) out[p] = u2v{w[p][0], w[p][1]};
   }
 }
 
 // ---------------------------------------------------------------------------
-// tiles in LDS: [rows][D] in units of 4 elements, the unit index of a row
-// XORed with a function of the row. 8-byte units (16-bit elements): 32 rows at
-// one unit index, and 4 rows at 8 consecutive ones, each cover all 64 banks.
-// 16-byte units (fp32): 16 rows at one unit index do.
+// tiles in LDS: [rows][D], D a power of two, in 16-byte units, the unit index of
+// a row XORed with a function of the row. 16 rows at one unit index cover all 64
+// banks (row fragments), and with 16-bit elements so do 4 rows at 4 consecutive
+// ones (column fragments).
+//
+// The function is linear over XOR, so an offset splits into a part of the lane,
+// worked out once per kernel, and a constant: for rows and units whose bits do
+// not overlap, offset(r | R, u ^ U) = (offset(r, u) ^ shift(R, U)) + R D.
 // ---------------------------------------------------------------------------
+template <class TM>
+constexpr int kUnit = 16 / (int)sizeof(TM);  // elements of a unit
+
 template <class TM, int D>
-__device__ __forceinline__ int swizzle(int row) {
-  constexpr int U = D / 4;
+__device__ __forceinline__ constexpr int swizzle(int row) {
+  constexpr int U = D / kUnit<TM>;
   static_assert(U == 8 || U == 16 || U == 32, "tile width");
-  if constexpr (sizeof(TM) == 2) {
-    constexpr int drop = U >= 32 ? 0 : (U == 16 ? 1 : 2);
-    return (((row & 3) >> drop) << 3) | ((row >> 2) & 7);
-  } else {
-    return U >= 16 ? (row & 15) : ((row >> 1) & 7);
-  }
+  if constexpr (U == 8) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
+  return ((row & 3) << 2) | ((row >> 2) & 3);
 }
 template <class TM, int D>
 __device__ __forceinline__ int unit_at(int row, int unit) {  // element offset of a unit
-  return row * D + ((unit ^ swizzle<TM, D>(row)) << 2);
+  return row * D + (unit ^ swizzle<TM, D>(row)) * kUnit<TM>;
+}
+template <class TM, int D>
+__device__ __forceinline__ int moved(int off, int row, int unit) {
+  return (off ^ ((unit ^ swizzle<TM, D>(row)) * kUnit<TM>)) + row * D;
+}
+// Element (row, col) for a lane's col: the offset of its unit and the place in it.
+template <class TM, int D>
+__device__ __forceinline__ int cell_at(int row, int col) {
+  return unit_at<TM, D>(row, col / kUnit<TM>) + col % kUnit<TM>;
 }
 
-// rows row0 + (l & 31), contraction axis along the row at k0 (32-wide tiles)
-template <class TM, int D>
-__device__ __forceinline__ typename Math<TM>::Frag row_frag32(const TM* tile, int row0, int k0, int l) {
-  typedef typename Math<TM>::Unit Unit;
-  const int row = row0 + (l & 31), u = (k0 >> 2) + (l >> 5);
-  const Unit a = *(const Unit*)(tile + unit_at<TM, D>(row, u));
-  const Unit b = *(const Unit*)(tile + unit_at<TM, D>(row, u + 2));
-  return Math<TM>::join(a, b);
+// Row fragments: R-wide tiles (R = 32 or 16), contraction axis along the rows.
+// Lane offset, and the fragment of rows row0 (a multiple of R) + l % R, entries
+// k0 + 8 (l / R) .. + 7, k0 a multiple of the step (16 or 32).
+template <class TM, int D, int R>
+__device__ __forceinline__ int row_lane() {
+  const int l = lane_id();
+  return unit_at<TM, D>(l % R, l / R * (8 / kUnit<TM>));
 }
-// rows row0 + (l & 15), 32 axis entries from k0 (16-wide tiles); the four lane
-// groups take units {0,2}, {4,6}, {1,3}, {5,7}, which keeps a read of 32 lanes
-// on distinct banks
 template <class TM, int D>
-__device__ __forceinline__ typename Math<TM>::Frag row_frag16(const TM* tile, int row0, int k0, int l) {
-  typedef typename Math<TM>::Unit Unit;
-  const int row = row0 + (l & 15), q = l >> 4;
-  const int u = (k0 >> 2) + ((q & 1) << 2) + (q >> 1);
-  const Unit a = *(const Unit*)(tile + unit_at<TM, D>(row, u));
-  const Unit b = *(const Unit*)(tile + unit_at<TM, D>(row, u + 2));
-  return Math<TM>::join(a, b);
+__device__ __forceinline__ typename Math<TM>::Frag row_frag(const TM* tile, int off, int row0, int k0) {
+  const int u = k0 / kUnit<TM>;
+  if constexpr (sizeof(TM) == 2) {
+    return *(const bf8*)(tile + moved<TM, D>(off, row0, u));
+  } else {
+    const f4v a = *(const f4v*)(tile + moved<TM, D>(off, row0, u));
+    const f4v b = *(const f4v*)(tile + moved<TM, D>(off, row0, u + 1));
+    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
+  }
 }
-// columns col0 + (l & 31), contraction axis down the rows from row0 (a 16-step)
-template <class TM, int D>
-__device__ __forceinline__ typename Math<TM>::Frag col_frag32(const TM* tile, int row0, int col0, int l) {
-  const int h = l >> 5;
+// Entry of a state's 32 rows that row m of its accumulators holds: bits 2 and 3
+// change places.
+__device__ __forceinline__ constexpr int state_row(int m) { return (m & ~12) | ((m & 4) << 1) | ((m & 8) >> 1); }
+
+// Column fragments: 32-wide tiles, contraction axis down the rows row0 + 8 h ..
+// + 7, row0 a multiple of 16. Columns col0 (a multiple of 32) + l % 32, or, as
+// rows of a state (STATE), col0 + state_row(l % 32).
+template <class TM, int D, bool STATE>
+__device__ __forceinline__ int col_lane() {
+  const int l = lane_id(), h = l >> 5;
   if constexpr (sizeof(TM) == 2) {
     // a transposing read: each 16 lanes read 4 rows x 16 columns, lane i of
     // them 8 bytes of row i / 4, and get column i of the four rows
-    typedef __attribute__((address_space(3))) s4v* lds4;
-    const int row = row0 + 4 * h + ((l & 15) >> 2);
-    const int u = (col0 >> 2) + ((l >> 4) & 1) * 4 + (l & 3);
-    const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + unit_at<TM, D>(row, u)));
-    const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + unit_at<TM, D>(row + 8, u)));
-    return Math<TM>::join(__builtin_bit_cast(bf4, a), __builtin_bit_cast(bf4, b));
+    const int four = STATE ? ((l & 1) << 1) | ((l & 2) >> 1) : l & 3;  // of the 16 columns
+    return unit_at<TM, D>(8 * h + ((l & 15) >> 2), ((l >> 4) & 1) * 2 + (four >> 1)) + (four & 1) * 4;
   } else {
-    const int c = col0 + (l & 31);
+    return cell_at<TM, D>(8 * h, STATE ? state_row(l & 31) : l & 31);
+  }
+}
+template <class TM, int D>
+__device__ __forceinline__ typename Math<TM>::Frag col_frag(const TM* tile, int off, int row0, int col0) {
+  if constexpr (sizeof(TM) == 2) {
+    typedef __attribute__((address_space(3))) s4v* lds4;
+    const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + moved<TM, D>(off, row0, col0 / 8)));
+    const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + moved<TM, D>(off, row0 + 4, col0 / 8)));
+    return __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
+  } else {
     f8v f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int row = row0 + 4 * h + (e & 3) + ((e >> 2) << 3);
-      f[e] = tile[unit_at<TM, D>(row, c >> 2) + (c & 3)];
-    }
+    for (int e = 0; e < 8; ++e) f[e] = tile[moved<TM, D>(off, row0 + e, col0 / 4)];
     return f;
   }
 }
@@ -207,12 +257,22 @@ struct TileRegs {
   static_assert(C * (D / 8) % NT == 0, "tile split");
   Raw<TIn> r[N];
 
-  __device__ __forceinline__ void load(const TIn* base, int64_t st, int d, int nrows, int tid) {
-    asm volatile("" : "+v"(tid));  // addresses are built anew for every chunk
-    constexpr int STEP = NT / (D / 8);  // rows between a thread's loads
-    static_assert(NT % (D / 8) == 0, "rows per pass");
+  static constexpr int STEP = NT / (D / 8);  // rows between a thread's groups
+  static_assert(NT % (D / 8) == 0 && STEP >= 8, "rows per pass");
+
+  __device__ __forceinline__ void load(const TIn* base, int64_t st, int d, int nrows) {
+    const int tid = fresh_thread();  // addresses are built anew for every chunk
     const int row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
     const TIn* p = base + (int64_t)row0 * st + c;
+    if (nrows >= C && d == D) {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        r[i].w[0] = *(const u4v*)p;
+        if constexpr (sizeof(TIn) == 4) r[i].w[1] = *(const u4v*)(p + 4);
+        p += STEP * st;
+      }
+      return;
+    }
     const int n = c < d ? nrows : 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
@@ -226,27 +286,25 @@ struct TileRegs {
     }
   }
   template <class TM>
-  __device__ __forceinline__ void store(TM* tile, int tid) const {
-    asm volatile("" : "+v"(tid));
-    typedef typename Math<TM>::Unit Unit;
+  __device__ __forceinline__ void store(TM* tile) const {
+    const int tid = fresh_thread();
+    const int off = unit_at<TM, D>(tid / (D / 8), (tid % (D / 8)) * (8 / kUnit<TM>));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int e = tid + i * NT, row = e / (D / 8), u = (e % (D / 8)) * 2;
-      Unit a, b;
-      if constexpr (sizeof(TIn) == 4) {
-        a = __builtin_bit_cast(f4v, r[i].w[0]);
-        b = __builtin_bit_cast(f4v, r[i].w[1]);
-      } else if constexpr (sizeof(TM) == 4) {  // 16-bit input, fp32 math: widened exactly
-        const f8v f = __builtin_convertvector(__builtin_bit_cast(h8, r[i].w[0]), f8v);
-        a = __builtin_shufflevector(f, f, 0, 1, 2, 3);
-        b = __builtin_shufflevector(f, f, 4, 5, 6, 7);
+      TM* a = tile + moved<TM, D>(off, i * STEP, 0);
+      if constexpr (sizeof(TM) == 2) {
+        *(u4v*)a = r[i].w[0];
       } else {
-        const bf8 f = __builtin_bit_cast(bf8, r[i].w[0]);
-        a = __builtin_shufflevector(f, f, 0, 1, 2, 3);
-        b = __builtin_shufflevector(f, f, 4, 5, 6, 7);
+        TM* b = tile + moved<TM, D>(off, i * STEP, 1);
+        if constexpr (sizeof(TIn) == 4) {
+          *(u4v*)a = r[i].w[0];
+          *(u4v*)b = r[i].w[1];
+        } else {  // 16-bit input, fp32 math: widened exactly
+          const f8v f = __builtin_convertvector(__builtin_bit_cast(h8, r[i].w[0]), f8v);
+          *(f4v*)a = __builtin_shufflevector(f, f, 0, 1, 2, 3);
+          *(f4v*)b = __builtin_shufflevector(f, f, 4, 5, 6, 7);
+        }
       }
-      *(Unit*)(tile + unit_at<TM, D>(row, u)) = a;
-      *(Unit*)(tile + unit_at<TM, D>(row, u + 1)) = b;
     }
   }
 };
@@ -260,8 +318,8 @@ struct TileRegs {
 template <int C>
 struct Decays {
   double b[C];   // inclusive cumulative sum
-  float up[C];   // e^{b_t}
-  float dn[C];   // e^{b_C - b_t}
+  float out[C];  // what a step's product with the state is multiplied by
+  float in[C];   // what a step's value is multiplied by on its way into the state
   float all;     // e^{b_C}
   float pad[3];
 };
@@ -291,16 +349,19 @@ __device__ __forceinline__ double log2_decay(float g) {
   return (double)(g < -1e5f ? -1e5f : g) * 1.4426950408889634074;
 }
 
-// by one wave: lane t holds g of step t (0 past the chunk's last step)
-template <int C>
-__device__ __forceinline__ double write_decays(Decays<C>& dst, float g) {
+// By one wave: lane t holds g of step t (0 past the chunk's last step). The
+// outputs of a forward pass take e^{b} and the scale, its state e^{b_C - b}; the
+// adjoint (REV) has them the other way round.
+template <int C, bool REV>
+__device__ __forceinline__ double write_decays(Decays<C>& dst, float g, float scale) {
   const int l = lane_id();
   const double b = wave_cumsum(l < C ? log2_decay(g) : 0.0);
   const double all = __shfl(b, C - 1);
   if (l < C) {
+    const float up = exp2_fast((float)b), dn = exp2_fast((float)(all - b));
     dst.b[l] = b;
-    dst.up[l] = exp2_fast((float)b);
-    dst.dn[l] = exp2_fast((float)(all - b));
+    dst.out[l] = REV ? dn : up * scale;
+    dst.in[l] = REV ? up * scale : dn;
     if (l == 0) dst.all = exp2_fast((float)all);
   }
   return all;

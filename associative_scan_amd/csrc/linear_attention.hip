@@ -15,11 +15,11 @@ namespace la {
 template <class TIn, class TM, int DX, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   constexpr int C = kChunk<TM>, DZ = NW * 32, NT = NW * 64, NP = kPiecesP<TM>;
-  __shared__ __align__(16) TM Q[C * DX];
+  __shared__ __align__(16) TM Q[C * (DX > DZ ? DX : DZ)];  // and then the chunk's outputs
   __shared__ __align__(16) TM K[C * DX];
   __shared__ __align__(16) TM V[C * DZ];
   __shared__ __align__(16) TM P[NP * C * C];
-  __shared__ __align__(16) Decays<C> dec;
+  __shared__ __align__(16) Decays<C> dec[2];
   const LaProblem& pr = a.pr;
   const int tid = threadIdx.x, wave = tid >> 6, z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
@@ -44,26 +44,41 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   TileRegs<TIn, C, DZ, NT> rv;
   float rg = 0.f;
   auto fetch = [&](int t) {
-    rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t, tid);
-    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t, tid);
-    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t, tid);
-    if (wave == 0) rg = load_gate(gp, pr.gst, t, sp.n);
+    rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t);
+    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t);
+    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t);
+    if (wave == NW - 1) rg = load_gate(gp, pr.gst, t, sp.n);
   };
-  fetch(0);
-  for (int t = 0; t < sp.n; t += C) {
-    rq.store(Q, tid);
-    rk.store(K, tid);
-    rv.store(V, tid);
-    if (wave == 0) write_decays<C>(dec, rg);
-    __syncthreads();
-    if (t + C < sp.n) fetch(t + C);
-    scores<TM, C, DX, NP, false>(Q, K, P, dec, pr.scale, wave, NW);
+  const LaneOffsets<TM, C, DX, DZ> at(z0);
+  if (sp.n > 0) {
+    fetch(0);
+    rq.store(Q);
+    rk.store(K);
+    rv.store(V);
+    if (wave == NW - 1) write_decays<C, false>(dec[0], rg, pr.scale);
+  }
+  __syncthreads();
+  for (int t = 0, cur = 0; t < sp.n; t += C, cur ^= 1) {
+    const bool more = t + C < sp.n;
+    if (more) fetch(t + C);
+    scores<TM, C, DX, NP, false>(Q, K, at.x16, P, dec[cur], pr.scale, wave, NW);
     f16v acc[C / 32];
-    from_state<TM, C, DX, kPiecesX<TM>>(Q, S, acc);
-    scale_rows<C>(acc, dec.up, pr.scale);
+    from_state<TM, C, DX, kPiecesX<TM>>(Q, at.x32, S, acc);
+    scale_rows<C>(acc, dec[cur].out);
     __syncthreads();
-    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(K, V, P, dec, 1.f, z0, S, acc);
-    store_rows<TIn, C>(acc, op + t * ost, ost, sp.n - t, pr.Dv, z0);
+    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(K, V, P, dec[cur], at, S, acc);
+    if (more && wave == NW - 1) write_decays<C, false>(dec[cur ^ 1], rg, pr.scale);
+    rows_to_lds<TIn, C, DZ>(acc, (TIn*)Q, z0);
+    __syncthreads();
+    OutRegs<TIn, C, DZ, NT> out;
+    out.take((const TIn*)Q);
+    if constexpr (DX != DZ || sizeof(TIn) != sizeof(TM)) __syncthreads();
+    if (more) {
+      rq.store(Q);
+      rk.store(K);
+      rv.store(V);
+    }
+    out.put(op + t * ost, ost, sp.n - t, pr.Dv);
     __syncthreads();
   }
   if (sp.is_last && a.ht)
@@ -126,19 +141,30 @@ hipError_t launch_join(const LaProblem& p, bool rev, const float* outer, float* 
 }
 
 // Steps per span. A workgroup per head and sequence needs no second pass over
-// k and v, but fills the card only with many heads and sequences.
+// k and v, but fills the card only with many heads and sequences; with fewer, the
+// rows are cut so that the workgroups fill the card's 512 places (two on each of
+// 256 CUs) a whole number of times, as far as spans of 256 steps allow.
 void plan(LaProblem& p, bool backward) {
-  const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H;
-  const int64_t want = 768 / rows > 0 ? 768 / rows : 1;  // spans per row
-  int64_t span = (p.T + want - 1) / want;
-  span = (span + 63) / 64 * 64;
-  if (span < 256) span = 256;
-  p.span = span;
+  const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H, places = 512;
+  int64_t best = p.T, best_cost = INT64_MAX;
+  for (int64_t r = 1; r <= 4; ++r) {
+    const int64_t n = places * r / rows;  // spans per row that fill r rounds
+    if (n < 1) continue;
+    int64_t span = ((p.T + n - 1) / n + 63) / 64 * 64;
+    if (span < 256) span = 256;
+    const int64_t blocks = (p.T + span - 1) / span * rows;
+    const int64_t cost = (blocks + places - 1) / places * (span + 64);  // and a chunk's time to start up
+    if (cost < best_cost) {
+      best_cost = cost;
+      best = span;
+    }
+  }
+  p.span = best;
   if (p.cu) {
     p.spans = 0;
-    p.slots = (int32_t)(p.T / span + p.nseg + 1);
+    p.slots = (int32_t)(p.T / best + p.nseg + 1);
   } else {
-    p.spans = (int32_t)((p.T + span - 1) / span);
+    p.spans = (int32_t)((p.T + best - 1) / best);
     p.slots = (int32_t)(p.B * p.spans);
   }
 }

@@ -69,24 +69,25 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   TileRegs<TIn, C, DZ, NT> rk, rq;
   float rg = 0.f;
   auto fetch = [&](int t) {
-    ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t, tid);
-    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t, tid);
-    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t, tid);
-    if constexpr (DG) rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t, tid);
+    ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t);
+    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t);
+    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t);
+    if constexpr (DG) rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t);
     if (wave == 0) rg = load_gate(gp, pr.gst, t, sp.n);
   };
   fetch(0);
+  const LaneOffsets<TM, C, DX, DZ> at(z0);
   for (int t = 0; t < sp.n; t += C) {
-    ro.store(O, tid);
-    rv.store(V, tid);
-    rk.store(K, tid);
-    if constexpr (DG) rq.store(P, tid);
-    if (wave == 0) write_decays<C>(dec, rg);
+    ro.store(O);
+    rv.store(V);
+    rk.store(K);
+    if constexpr (DG) rq.store(P);
+    if (wave == 0) write_decays<C, false>(dec, rg, pr.scale);
     __syncthreads();
     if (t + C < sp.n) fetch(t + C);
     f16v acc[C / 32];
-    from_state<TM, C, DX, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(O, S, acc);
-    scale_rows<C>(acc, dec.up, pr.scale);
+    from_state<TM, C, DX, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(O, at.x32, S, acc);
+    scale_rows<C>(acc, dec.out);
     if constexpr (DG) {
       row_dots<TM, C, DZ>(acc, P, z0, part[wave]);
       __syncthreads();
@@ -97,12 +98,12 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
         rows[row0 + (int64_t)(t + tid) * pr.H] = s;
       }
     }
-    scores<TM, C, DX, NP, false>(O, V, P, dec, pr.scale, wave, NW);
+    scores<TM, C, DX, NP, false>(O, V, at.x16, P, dec, pr.scale, wave, NW);
     __syncthreads();
-    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(V, K, P, dec, 1.f, z0, S, acc);
-    const int64_t at = row0 * pr.Dk + (int64_t)t * ost;
-    if (shared) store_rows<float, C>(acc, a.dq_part + at, ost, sp.n - t, pr.Dk, z0);
-    else store_rows<TIn, C>(acc, (TIn*)a.dq + at, ost, sp.n - t, pr.Dk, z0);
+    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(V, K, P, dec, at, S, acc);
+    const int64_t o = row0 * pr.Dk + (int64_t)t * ost;
+    if (shared) store_rows<float, C>(acc, a.dq_part + o, ost, sp.n - t, pr.Dk, z0);
+    else store_rows<TIn, C>(acc, (TIn*)a.dq + o, ost, sp.n - t, pr.Dk, z0);
     __syncthreads();
   }
   if constexpr (DG) {  // <Lam, S> at the end of the span
@@ -171,20 +172,21 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
   TileRegs<TIn, C, D, NT> rq, rk, rv, ro;
   float rg = 0.f;
   auto fetch = [&](int t) {
-    rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t, tid);
-    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t, tid);
-    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t, tid);
-    ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t, tid);
+    rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t);
+    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t);
+    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t);
+    ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t);
     if (wave == 0) rg = load_gate(gp, pr.gst, t, sp.n);
   };
   const int last = sp.n > 0 ? (sp.n - 1) / C * C : -C;
   if (last >= 0) fetch(last);
+  const LaneOffsets<TM, C, D, D> at(z0);
   for (int t = last; t >= 0; t -= C) {
-    rq.store(Q, tid);
-    rk.store(K, tid);
-    rv.store(V, tid);
-    ro.store(O, tid);
-    if (wave == 0) write_decays<C>(dec, rg);
+    rq.store(Q);
+    rk.store(K);
+    rv.store(V);
+    ro.store(O);
+    if (wave == 0) write_decays<C, true>(dec, rg, pr.scale);
     __syncthreads();
     if (t > 0) fetch(t - C);
     {  // scores of both roles, and W's sums over i and over j
@@ -193,8 +195,8 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
         int rt, ct;
         tile_of<C, true>(i, rt, ct);
         const f4v d = decay_tile<C, true>(dec, rt, ct, l);
-        f4v x = score_tile<TM, D>(K, Q, rt, ct, l);
-        f4v y = score_tile<TM, D>(V, O, rt, ct, l);
+        f4v x = score_tile<TM, D>(K, Q, at.x16, rt, ct);
+        f4v y = score_tile<TM, D>(V, O, at.x16, rt, ct);
         float row[4], col = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -220,8 +222,8 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
       }
     }
     f16v acc[C / 32];
-    from_state<TM, C, D, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(X, S, acc);
-    scale_rows<C>(acc, dec.dn, 1.f);
+    from_state<TM, C, D, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(X, at.x32, S, acc);
+    scale_rows<C>(acc, dec.out);
     if constexpr (DG)
       if (is_dk) row_dots<TM, C, D>(acc, K, z0, part[wave - NW]);
     __syncthreads();
@@ -239,11 +241,11 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
         }
         rows[row0 + (int64_t)(t + tid) * pr.H] = s;
       }
-    within_chunk<TM, C, D, D, NP, kPiecesZ<TM>, true>(Y, Z, P[is_dk], dec, pr.scale, z0, S, acc);
+    within_chunk<TM, C, D, D, NP, kPiecesZ<TM>, true>(Y, Z, P[is_dk], dec, at, S, acc);
     if (is_dk) {
-      const int64_t at = row0 * pr.Dk + (int64_t)t * kst;
-      if (shared) store_rows<float, C>(acc, a.dk_part + at, kst, sp.n - t, pr.Dk, z0);
-      else store_rows<TIn, C>(acc, (TIn*)a.dk + at, kst, sp.n - t, pr.Dk, z0);
+      const int64_t o = row0 * pr.Dk + (int64_t)t * kst;
+      if (shared) store_rows<float, C>(acc, a.dk_part + o, kst, sp.n - t, pr.Dk, z0);
+      else store_rows<TIn, C>(acc, (TIn*)a.dk + o, kst, sp.n - t, pr.Dk, z0);
     } else {
       store_rows<TIn, C>(acc, (TIn*)a.dv + row0 * pr.Dv + (int64_t)t * vst, vst, sp.n - t, pr.Dv, z0);
     }
