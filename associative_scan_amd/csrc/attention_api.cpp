@@ -20,6 +20,7 @@ mscan_status hip_status(hipError_t e) { return (mscan_status)mscan::status_of_hi
 constexpr int64_t kMaxHeadDim = 128;
 // A launch counts its work-items in 32 bits, and a workgroup has up to 512.
 constexpr int64_t kMaxBlocks = (int64_t)1 << 22;
+constexpr int64_t kMaxHeads = (int64_t)1 << 16;  // 64 rows of [H][128] fp32 stay below 2^31 bytes
 
 mscan_status check(const mscan_attention* p) {
   if (!p) return MSCAN_ERR_INVALID;
@@ -28,7 +29,7 @@ mscan_status check(const mscan_attention* p) {
   if (p->cu_seqlens ? (p->B != 1 || ((uintptr_t)p->cu_seqlens & 3u)) : (p->nseg != p->B)) return MSCAN_ERR_INVALID;
   if (p->Dk < 1 || p->Dv < 1) return MSCAN_ERR_INVALID;
   if (p->Dk % 8 || p->Dv % 8 || p->Dk > kMaxHeadDim || p->Dv > kMaxHeadDim) return MSCAN_ERR_UNSUPPORTED;
-  if (p->B > kMaxBlocks || p->H > kMaxBlocks || p->nseg > kMaxBlocks) return MSCAN_ERR_UNSUPPORTED;
+  if (p->B > kMaxBlocks || p->H > kMaxHeads || p->nseg > kMaxBlocks) return MSCAN_ERR_UNSUPPORTED;
   return MSCAN_OK;
 }
 
@@ -63,6 +64,8 @@ mscan_status heads(const mscan_heads* x, int dtype, int share, int d, Heads& out
   const int64_t unit = dtype == MSCAN_F32 ? 4 : 8;
   for (int i = 0; i < 3; ++i)
     if (x->strides[i] < 0 || x->strides[i] % unit) return MSCAN_ERR_INVALID;
+  // the kernels address the rows of a chunk by 32-bit byte offsets
+  if (x->strides[1] > ((int64_t)1 << 23)) return MSCAN_ERR_UNSUPPORTED;
   out = Heads{x->p, x->strides[0], x->strides[1], x->strides[2], share, d};
   return MSCAN_OK;
 }

@@ -23,8 +23,6 @@ constexpr int kPiecesX = sizeof(TM) == 2 ? 2 : 1;
 template <class TM>
 constexpr int kPiecesXExact = sizeof(TM) == 2 ? 3 : 1;
 
-__device__ __forceinline__ int acc_row(int r) { return ((r >> 2) << 3) + ((lane_id() >> 5) << 2) + (r & 3); }
-
 // A lane's offsets into the tiles (see la_device.hpp).
 template <class TM, int C, int DX, int DZ>
 struct LaneOffsets {
@@ -37,21 +35,23 @@ struct LaneOffsets {
 // One 16 x 16 tile of the scores x_r . y_c, transposed: rows ct*16 + 4 (l / 16)
 // + i, i < 4, are steps c, column rt*16 + (l & 15) is step r.
 template <class TM, int DX>
-__device__ __forceinline__ f4v score_tile(const TM* X, const TM* Y, int x16, int rt, int ct) {
-  const TM* x = X + rt * 16 * DX;  // 16 rows leave the units' order as it is
-  const TM* y = Y + ct * 16 * DX;
-  typename Math<TM>::Frag xf[DX / 32], yf[DX / 32];
+struct ScoreFrags {
+  typename Math<TM>::Frag x[DX / 32], y[DX / 32];
+  __device__ __forceinline__ void read(const TM* X, const TM* Y, int x16, int rt, int ct) {
+    // 16 rows leave the units' order as it is
 #pragma unroll
-  for (int i = 0; i < DX / 32; ++i) {
-    yf[i] = row_frag<TM, DX>(y, x16, 0, i * 32);
-    xf[i] = row_frag<TM, DX>(x, x16, 0, i * 32);
+    for (int i = 0; i < DX / 32; ++i) {
+      y[i] = row_frag<TM, DX>(Y + ct * 16 * DX, x16, 0, i * 32);
+      x[i] = row_frag<TM, DX>(X + rt * 16 * DX, x16, 0, i * 32);
+    }
   }
-  step_fence();
-  f4v acc = {0.f, 0.f, 0.f, 0.f};
+  __device__ __forceinline__ f4v product() const {
+    f4v acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-  for (int i = 0; i < DX / 32; ++i) acc = Math<TM>::mma16(yf[i], xf[i], acc);
-  return acc;
-}
+    for (int i = 0; i < DX / 32; ++i) acc = Math<TM>::mma16(y[i], x[i], acc);
+    return acc;
+  }
+};
 // The decays of such a tile: e^{b_r - b_c} for c <= r (REV: e^{b_c - b_r} for
 // c >= r), zero elsewhere.
 template <int C, bool REV>
@@ -97,18 +97,33 @@ __device__ __forceinline__ void tile_of(int i, int& rt, int& ct) {
     }
   }
 }
-template <class TM, int C, int DX, int NP, bool REV>
+template <class TM, int C, int DX, int NP, bool REV, int WAVES>
 __device__ __forceinline__ void scores(const TM* X, const TM* Y, int x16, TM* P, const Decays<C>& d, float scale,
-                                       int wave, int nwaves) {
+                                       int wave) {
   const int l = fresh_lane();
-  for (int i = wave; i < kTiles<C>; i += nwaves) {
-    int rt, ct;
-    tile_of<C, REV>(i, rt, ct);
+  x16 = fresh(x16);
+  constexpr int N = (kTiles<C> + WAVES - 1) / WAVES;
+  ScoreFrags<TM, DX> f[2];
+  int rt, ct;
+  tile_of<C, REV>(wave, rt, ct);
+  if (wave < kTiles<C>) f[0].read(X, Y, x16, rt, ct);
+#pragma unroll
+  for (int j = 0; j < N; ++j) {
+    const int i = wave + j * WAVES;
+    if (i >= kTiles<C>) break;
+    int rn = 0, cn = 0;
+    if (i + WAVES < kTiles<C>) {  // the next tile's reads before this one's product
+      tile_of<C, REV>(i + WAVES, rn, cn);
+      f[(j + 1) & 1].read(X, Y, x16, rn, cn);
+    }
     const f4v dec = decay_tile<C, REV>(d, rt, ct, l);
-    f4v acc = score_tile<TM, DX>(X, Y, x16, rt, ct);
+    step_fence();
+    f4v acc = f[j & 1].product();
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = dec[e] != 0.f ? acc[e] * (dec[e] * scale) : 0.f;
     put_tile<TM, C, NP>(P, acc, rt, ct, l);
+    rt = rn;
+    ct = cn;
   }
 }
 
@@ -133,46 +148,50 @@ __device__ __forceinline__ void interleave() {
   }
 }
 
-// acc[rt] = rows of X times the state. A step issues the reads of the next one
-// and splits the next one's state between its own products.
+// acc[rt] = rows rt*32 .. + 31 of X times the state, transposed: lane l has row
+// l % 32, register 4 a + i the wave's column 8 a + 4 (l / 32) + i. Reads run two
+// steps ahead, and a step splits the next one's state between its products.
 template <class TM, int C, int DX, int NS>
 __device__ __forceinline__ void from_state(const TM* X, int x32, const f16v (&S)[DX / 32], f16v (&acc)[C / 32]) {
+  constexpr int RT = C / 32, N = DX / 16;
+  x32 = fresh(x32);
 #pragma unroll
-  for (int rt = 0; rt < C / 32; ++rt)
+  for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[rt][r] = 0.f;
-  typename Math<TM>::Frag x[2][C / 32], piece[2][NS];
+  typename Math<TM>::Frag x[3][RT], piece[2][NS];
 #pragma unroll
-  for (int rt = 0; rt < C / 32; ++rt) x[0][rt] = row_frag<TM, DX>(X, x32, rt * 32, 0);
+  for (int s = 0; s < 2; ++s)
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) x[s][rt] = row_frag<TM, DX>(X, x32, rt * 32, s * 16);
   split8<TM, NS>(state8<DX / 32>(S, 0), piece[0]);
 #pragma unroll
-  for (int s = 0; s < DX / 16; ++s) {
+  for (int s = 0; s < N; ++s) {
     step_fence();
-    if (s + 1 < DX / 16) {
+    if (s + 2 < N) {
 #pragma unroll
-      for (int rt = 0; rt < C / 32; ++rt) x[(s + 1) & 1][rt] = row_frag<TM, DX>(X, x32, rt * 32, (s + 1) * 16);
+      for (int rt = 0; rt < RT; ++rt) x[(s + 2) % 3][rt] = row_frag<TM, DX>(X, x32, rt * 32, (s + 2) * 16);
     }
     step_fence();
 #pragma unroll
     for (int p = 0; p < NS; ++p)
 #pragma unroll
-      for (int rt = 0; rt < C / 32; ++rt) acc[rt] = Math<TM>::mma32(x[s & 1][rt], piece[s & 1][p], acc[rt]);
-    if (s + 1 < DX / 16) split8<TM, NS>(state8<DX / 32>(S, s + 1), piece[(s + 1) & 1]);
-    if constexpr (sizeof(TM) == 2) interleave<NS * (C / 32), 7>();
+      for (int rt = 0; rt < RT; ++rt) acc[rt] = Math<TM>::mma32(piece[s & 1][p], x[s % 3][rt], acc[rt]);
+    if (s + 1 < N) split8<TM, NS>(state8<DX / 32>(S, s + 1), piece[(s + 1) & 1]);
+    if constexpr (sizeof(TM) == 2) interleave<NS * RT, 7>();
   }
+  step_fence();
 }
 // rows of acc times f[row]
 template <int C>
 __device__ __forceinline__ void scale_rows(f16v (&acc)[C / 32], const float* f) {
-  const int h4 = (fresh_lane() >> 5) << 2;
+  const int l = fresh_lane() & 31;
 #pragma unroll
-  for (int rt = 0; rt < C / 32; ++rt)
+  for (int rt = 0; rt < C / 32; ++rt) {
+    const float w = f[rt * 32 + l];
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-      const f4v w = *(const f4v*)(f + rt * 32 + a * 8 + h4);
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[rt][a * 4 + i] *= w[i];
-    }
+    for (int r = 0; r < 16; ++r) acc[rt][r] *= w;
+  }
 }
 template <int NT>
 __device__ __forceinline__ void scale_state(f16v (&S)[NT], float f) {
@@ -203,35 +222,45 @@ __device__ __forceinline__ void within_chunk(const TM* Y, const TM* Z, const TM*
   typedef typename Math<TM>::Frag Frag;
   constexpr int RT = C / 32, KP = NP > 0 ? NP : 1, JS = C / 16;
   Frag z[2], y[DX / 32], pf[RT][KP], piece[2][NS];
+  const int oy = fresh(at.y), oz = fresh(at.z), op = fresh(at.p);
   const auto inside = [](int rt, int js) { return REV ? js * 16 >= rt * 32 : js * 16 < rt * 32 + 32; };
-  z[0] = col_frag<TM, DZ>(Z, at.z, 0, 0);
-  if (JS > 1) z[1] = col_frag<TM, DZ>(Z, at.z, 16, 0);
+  const auto read_y = [&](int js) {
+#pragma unroll
+    for (int t = 0; t < DX / 32; ++t) y[t] = col_frag<TM, DX>(Y, oy, js * 16, t * 32);
+  };
+  z[0] = col_frag<TM, DZ>(Z, oz, 0, 0);
+  read_y(0);
+  if (JS > 1) z[1] = col_frag<TM, DZ>(Z, oz, 16, 0);
   scale_state<DX / 32>(S, d.all);
   weigh<TM, NS>(z[0], d.in, 0, piece[0]);
 #pragma unroll
   for (int js = 0; js < JS; ++js) {
     step_fence();
+    // the scores' reads are covered by the state's products, the next step's
+    // reads of Y by the outputs'
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt)
       if (inside(rt, js))
 #pragma unroll
-        for (int p = 0; p < NP; ++p) pf[rt][p] = row_frag<TM, C>(P + p * C * C, at.p, rt * 32, js * 16);
-#pragma unroll
-    for (int t = 0; t < DX / 32; ++t) y[t] = col_frag<TM, DX>(Y, at.y, js * 16, t * 32);
+        for (int p = 0; p < NP; ++p) pf[rt][p] = row_frag<TM, C>(P + p * C * C, op, rt * 32, js * 16);
     step_fence();
-#pragma unroll
-    for (int p = 0; p < NP; ++p)
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        if (inside(rt, js)) acc[rt] = Math<TM>::mma32(pf[rt][p], z[js & 1], acc[rt]);
 #pragma unroll
     for (int p = 0; p < NS; ++p)
 #pragma unroll
       for (int t = 0; t < DX / 32; ++t) S[t] = Math<TM>::mma32(y[t], piece[js & 1][p], S[t]);
     if (js + 1 < JS) weigh<TM, NS>(z[(js + 1) & 1], d.in, js + 1, piece[(js + 1) & 1]);
-    if (js + 2 < JS) z[js & 1] = col_frag<TM, DZ>(Z, at.z, (js + 2) * 16, 0);
-    if constexpr (sizeof(TM) == 2) interleave<NS * (DX / 32) + NP, 5>();
+    if constexpr (sizeof(TM) == 2) interleave<NS * (DX / 32), 6>();
+    step_fence();
+    if (js + 1 < JS) read_y(js + 1);
+    step_fence();
+#pragma unroll
+    for (int p = 0; p < NP; ++p)
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt)
+        if (inside(rt, js)) acc[rt] = Math<TM>::mma32(z[js & 1], pf[rt][p], acc[rt]);
+    if (js + 2 < JS) z[js & 1] = col_frag<TM, DZ>(Z, oz, (js + 2) * 16, 0);
   }
+  step_fence();
 }
 
 // The wave's 32 columns of a state in memory: element (x, z) of the wave's
@@ -299,85 +328,119 @@ __device__ __forceinline__ float sum16(float x) {  // over the 16 lanes of a DPP
 // Sums over the wave's 32 columns of acc times the rows of a tile, to dst[C].
 template <class TM, int C, int D>
 __device__ __forceinline__ void row_dots(const f16v (&acc)[C / 32], const TM* tile, int z0, float* dst) {
-  const int l = fresh_lane(), h4 = (l >> 5) << 2, off = cell_at<TM, D>(h4, z0 + (l & 31));
-  constexpr int N = C / 4;  // values of a lane, halved by the exchange between DPP rows
-  float w[C / 2];
+  typedef TM four __attribute__((ext_vector_type(4)));
+  const int l = fresh_lane(), off = cell_at<TM, D>(l & 31, z0 + ((l >> 5) << 2));
 #pragma unroll
-  for (int i = 0; i < C / 2; ++i) {
-    const int row = (i >> 4) * 32 + (((i & 15) >> 2) << 3) + (i & 3);
-    w[i] = acc[i >> 4][i & 15] * (float)tile[moved<TM, D>(off, row, 0)];
-  }
-  float mine = 0.f;
+  for (int rt = 0; rt < C / 32; ++rt) {
+    float s = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    // the first DPP row of a pair sums value i, the second value i + N
-    const auto x = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, w[i]),
-                                                    __builtin_bit_cast(uint32_t, w[i + N]), false, false);
-    const float v = sum16(__builtin_bit_cast(float, (uint32_t)x[0]) + __builtin_bit_cast(float, (uint32_t)x[1]));
-    mine = (l & 15) == i ? v : mine;
+    for (int a = 0; a < 4; ++a) {
+      const f4v w = __builtin_convertvector(*(const four*)(tile + moved<TM, D>(off, rt * 32, a * 8 / kUnit<TM>)), f4v);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) s += acc[rt][a * 4 + i] * w[i];
+    }
+    s += __shfl_xor(s, 32);
+    if (l < 32) dst[rt * 32 + l] = s;
   }
-  const int i = (l & 15) + ((l >> 4) & 1) * N;
-  if ((l & 15) < N) dst[(i >> 4) * 32 + (((i & 15) >> 2) << 3) + h4 + (i & 3)] = mine;
 }
+// The same with rows from memory, read ahead in acc's own layout.
+template <class TIn, int C>
+struct RowRegs {
+  typedef TIn four __attribute__((ext_vector_type(4)));
+  four r[C / 32][4];
+  __device__ __forceinline__ void load(const TIn* base, int64_t st, int d, int n, int z0) {
+    const Window w = window<TIn, C>(base, st, d, n);
+    const int l = fresh_lane(), z = z0 + ((l >> 5) << 2);
+#pragma unroll
+    for (int rt = 0; rt < C / 32; ++rt) {
+      const uint32_t row = (uint32_t)(rt * 32 + (l & 31)) * (uint32_t)st;
+#pragma unroll
+      for (int a = 0; a < 4; ++a) {
+        const bool in = rt * 32 + (l & 31) < n && z + a * 8 < d;
+        const uint32_t off = in ? (row + z + a * 8) * (uint32_t)sizeof(TIn) : kOutside;
+        if constexpr (sizeof(TIn) == 4) r[rt][a] = __builtin_bit_cast(four, __builtin_amdgcn_raw_buffer_load_b128(w, off, 0, 0));
+        else r[rt][a] = __builtin_bit_cast(four, __builtin_amdgcn_raw_buffer_load_b64(w, off, 0, 0));
+      }
+    }
+  }
+  __device__ __forceinline__ void dots(const f16v (&acc)[C / 32], float* dst) const {
+    const int l = fresh_lane();
+#pragma unroll
+    for (int rt = 0; rt < C / 32; ++rt) {
+      float s = 0.f;
+#pragma unroll
+      for (int a = 0; a < 4; ++a)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s += acc[rt][a * 4 + i] * (float)r[rt][a][i];
+      s += __shfl_xor(s, 32);
+      if (l < 32) dst[rt * 32 + l] = s;
+    }
+  }
+};
 
 // Rows of an output: the wave's 32 columns of acc as TOut into a [C][D] array in
 // LDS, from there as whole 16-byte units to registers, and to [n][..][d] in
 // memory. A thread takes the units that TileRegs::store writes, so the next
 // chunk's tile of that shape can take the same place without a barrier. The
 // stores to memory come after the next tiles' waits for their loads, which would
-// otherwise wait for the stores too.
+// otherwise wait for the stores too; as streaming stores they leave the caches to
+// the inputs (prompts of 8 x 4096 steps: 180 us instead of 195).
 template <class TOut, int C, int D>
 __device__ __forceinline__ void rows_to_lds(const f16v (&acc)[C / 32], TOut* tile, int z0) {
-  const int l = fresh_lane(), off = cell_at<TOut, D>((l >> 5) << 2, z0 + (l & 31));
+  typedef TOut four __attribute__((ext_vector_type(4)));
+  const int l = fresh_lane(), off = cell_at<TOut, D>(l & 31, z0 + ((l >> 5) << 2));
 #pragma unroll
   for (int rt = 0; rt < C / 32; ++rt)
 #pragma unroll
-    for (int r = 0; r < 16; ++r)
-      tile[moved<TOut, D>(off, rt * 32 + ((r >> 2) << 3) + (r & 3), 0)] = (TOut)acc[rt][r];
+    for (int a = 0; a < 4; ++a) {
+      const f4v v = {acc[rt][a * 4], acc[rt][a * 4 + 1], acc[rt][a * 4 + 2], acc[rt][a * 4 + 3]};
+      *(four*)(tile + moved<TOut, D>(off, rt * 32, a * 8 / kUnit<TOut>)) = __builtin_convertvector(v, four);
+    }
 }
 template <class TOut, int C, int D, int NT>
 struct OutRegs {
   static constexpr int STEP = NT / (D / 8), N = C / STEP, W = sizeof(TOut) == 4 ? 2 : 1;
   u4v r[N][W];
   __device__ __forceinline__ void take(const TOut* tile) {
-    const int tid = fresh_thread();
-    const int off = unit_at<TOut, D>(tid / (D / 8), (tid % (D / 8)) * (8 / kUnit<TOut>));
+    const unsigned tid = fresh_thread();
+    const int off = unit_at<TOut, D>((int)(tid / (D / 8)), (int)(tid % (D / 8)) * (8 / kUnit<TOut>));
 #pragma unroll
     for (int i = 0; i < N; ++i)
 #pragma unroll
       for (int w = 0; w < W; ++w) r[i][w] = *(const u4v*)(tile + moved<TOut, D>(off, i * STEP, w));
   }
   __device__ __forceinline__ void put(TOut* out, int64_t st, int n, int d) const {
-    const int tid = fresh_thread(), row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
-    TOut* p = out + row0 * st + c;
-    if (c >= d) n = 0;
+    const Window w = window<TOut, C>(out, st, d, n);
+    const unsigned tid = fresh_thread(), row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
+    const uint32_t step = STEP * (uint32_t)st * sizeof(TOut);
+    uint32_t off = (int)c < d ? (row0 * (uint32_t)st + c) * sizeof(TOut) : kOutside;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      if (row0 + i * STEP < n) {
 #pragma unroll
-        for (int w = 0; w < W; ++w) *(u4v*)(p + w * 4) = r[i][w];
-      }
-      p += STEP * st;
+      for (int x = 0; x < W; ++x) __builtin_amdgcn_raw_buffer_store_b128(r[i][x], w, off + 16 * x, 0, 2);
+      off += step;
     }
   }
 };
-// The same straight from registers, two rows of 32 columns at a time.
+// The same straight from registers, four columns of a lane's row at a time.
 template <class TOut, int C>
 __device__ __forceinline__ void store_rows(const f16v (&acc)[C / 32], TOut* out, int64_t st, int n, int d, int z0) {
-  const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 2;
-  if (z >= d) return;
-  TOut* p = out + r0 * st + z;
+  typedef TOut four __attribute__((ext_vector_type(4)));
+  const Window w = window<TOut, C>(out, st, d, n);
+  const int l = fresh_lane(), z = z0 + ((l >> 5) << 2);
+  const uint32_t row = (uint32_t)(l & 31) * (uint32_t)st * sizeof(TOut);
 #pragma unroll
-  for (int rt = 0; rt < C / 32; ++rt)
+  for (int a = 0; a < 4; ++a) {
+    uint32_t off = z + a * 8 < d ? row + (z + a * 8) * (uint32_t)sizeof(TOut) : kOutside;
 #pragma unroll
-    for (int a = 0; a < 4; ++a) {
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        if (rt * 32 + a * 8 + i + r0 < n) *p = (TOut)acc[rt][a * 4 + i];
-        p += st;
-      }
-      p += 4 * st;
+    for (int rt = 0; rt < C / 32; ++rt) {
+      const f4v v = {acc[rt][a * 4], acc[rt][a * 4 + 1], acc[rt][a * 4 + 2], acc[rt][a * 4 + 3]};
+      const four x = __builtin_convertvector(v, four);
+      if constexpr (sizeof(TOut) == 4) __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4v, x), w, off, 0, 0);
+      else __builtin_amdgcn_raw_buffer_store_b64(__builtin_bit_cast(u2v, x), w, off, 0, 0);
+      off += 32 * (uint32_t)st * sizeof(TOut);
     }
+  }
 }
 
 template <class TIn>
@@ -403,7 +466,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
   __shared__ __align__(16) TM Y[C * DX];
   __shared__ __align__(16) TM Z[C * DZ];
   __shared__ __align__(16) Decays<C> dec;
-  const int tid = threadIdx.x, wave = tid >> 6, z0 = wave * 32;
+  const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
   const Span sp = find_span(pr, slot);
   if (sp.seq >= (pr.cu ? pr.nseg : (int)pr.B) || sp.n == 0 || (REV ? sp.is_first : sp.is_last)) return;

@@ -42,11 +42,20 @@ __device__ __forceinline__ int fresh_lane() {
   asm volatile("" : "+v"(l));
   return l;
 }
-__device__ __forceinline__ int fresh_thread() {
-  int t = (int)threadIdx.x;
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+__device__ __forceinline__ unsigned fresh_thread() {
+  unsigned t = threadIdx.x;
   asm volatile("" : "+v"(t));
   return t;
 }
+// The wave's index, known to be the same for its lanes.
+__device__ __forceinline__ int wave_id() { return __builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6)); }
+// Waits for what was read before a loop, once: its first use inside the loop
+// would otherwise wait in every turn, for the loads in flight there too.
+__device__ __forceinline__ void settle() { __builtin_amdgcn_s_waitcnt(0); }
 // Keeps the reads of later steps of a phase from being moved ahead, which
 // would hold their results in registers too.
 __device__ __forceinline__ void step_fence() { __builtin_amdgcn_sched_barrier(0); }
@@ -243,9 +252,22 @@ __device__ __forceinline__ typename Math<TM>::Frag col_frag(const TM* tile, int 
 }
 
 // ---------------------------------------------------------------------------
-// global memory -> registers -> LDS, 8 elements per thread and step. Rows at or
-// past nrows and columns at or past d (a multiple of 8) become zeros.
+// global memory -> registers -> LDS, 8 elements per thread and step, through a
+// bounded window on the chunk's rows: a read past the last row or the last column
+// (a multiple of 8) gives zeros and a write there is dropped, so neither needs a
+// branch, and the loads stay in flight across the chunk.
 // ---------------------------------------------------------------------------
+typedef __amdgpu_buffer_rsrc_t Window;
+constexpr uint32_t kOutside = 0x80000000u;  // past any window, also with a chunk's rows added
+
+// n rows of st elements of which d count, n <= C; base, st, d and n are uniform and
+// C rows span less than 2^31 bytes
+template <class T, int C>
+__device__ __forceinline__ Window window(const T* base, int64_t st, int d, int n) {
+  n = n < C ? n : C;
+  const int bytes = n > 0 ? ((n - 1) * (int)st + d) * (int)sizeof(T) : 0;
+  return __builtin_amdgcn_make_buffer_rsrc((void*)base, 0, bytes, 0x00020000);
+}
 template <class TIn>
 struct Raw {
   u4v w[sizeof(TIn) == 4 ? 2 : 1];
@@ -261,34 +283,23 @@ struct TileRegs {
   static_assert(NT % (D / 8) == 0 && STEP >= 8, "rows per pass");
 
   __device__ __forceinline__ void load(const TIn* base, int64_t st, int d, int nrows) {
-    const int tid = fresh_thread();  // addresses are built anew for every chunk
-    const int row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
-    const TIn* p = base + (int64_t)row0 * st + c;
-    if (nrows >= C && d == D) {
-#pragma unroll
-      for (int i = 0; i < N; ++i) {
-        r[i].w[0] = *(const u4v*)p;
-        if constexpr (sizeof(TIn) == 4) r[i].w[1] = *(const u4v*)(p + 4);
-        p += STEP * st;
-      }
-      return;
-    }
-    const int n = c < d ? nrows : 0;
+    const Window w = window<TIn, C>(base, st, d, nrows);
+    const unsigned tid = fresh_thread(), row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
+    const uint32_t step = STEP * (uint32_t)st * sizeof(TIn);
+    uint32_t off = (row0 * (uint32_t)st + c) * sizeof(TIn);
+    const int n = (int)c < d ? nrows - (int)row0 : 0;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      r[i].w[0] = u4v{0, 0, 0, 0};
-      if constexpr (sizeof(TIn) == 4) r[i].w[1] = u4v{0, 0, 0, 0};
-      if (row0 + i * STEP < n) {
-        r[i].w[0] = *(const u4v*)p;
-        if constexpr (sizeof(TIn) == 4) r[i].w[1] = *(const u4v*)(p + 4);
-      }
-      p += STEP * st;
+      const uint32_t o = i * STEP < n ? off : kOutside;  // rows may lie closer than d, at a stride of zero
+      r[i].w[0] = __builtin_amdgcn_raw_buffer_load_b128(w, o, 0, 0);
+      if constexpr (sizeof(TIn) == 4) r[i].w[1] = __builtin_amdgcn_raw_buffer_load_b128(w, o + 16, 0, 0);
+      off += step;
     }
   }
   template <class TM>
   __device__ __forceinline__ void store(TM* tile) const {
-    const int tid = fresh_thread();
-    const int off = unit_at<TM, D>(tid / (D / 8), (tid % (D / 8)) * (8 / kUnit<TM>));
+    const unsigned tid = fresh_thread();
+    const int off = unit_at<TM, D>((int)(tid / (D / 8)), (int)(tid % (D / 8)) * (8 / kUnit<TM>));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       TM* a = tile + moved<TM, D>(off, i * STEP, 0);

@@ -21,7 +21,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   __shared__ __align__(16) TM P[NP * C * C];
   __shared__ __align__(16) Decays<C> dec[2];
   const LaProblem& pr = a.pr;
-  const int tid = threadIdx.x, wave = tid >> 6, z0 = wave * 32;
+  const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
   const Span sp = find_span(pr, slot);
   const int64_t ost = (int64_t)pr.H * pr.Dv;
@@ -43,27 +43,34 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   TileRegs<TIn, C, DX, NT> rq, rk;
   TileRegs<TIn, C, DZ, NT> rv;
   float rg = 0.f;
-  auto fetch = [&](int t) {
+  // the next chunk's loads are issued in three places: all at once they hold up
+  // the waves for as long as the memory pipeline takes to accept them
+  const auto fetch_q = [&](int t) {
     rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t);
-    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t);
-    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t);
     if (wave == NW - 1) rg = load_gate(gp, pr.gst, t, sp.n);
   };
+  const auto fetch_k = [&](int t) { rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t); };
+  const auto fetch_v = [&](int t) { rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t); };
   const LaneOffsets<TM, C, DX, DZ> at(z0);
   if (sp.n > 0) {
-    fetch(0);
+    fetch_q(0);
+    fetch_k(0);
+    fetch_v(0);
     rq.store(Q);
     rk.store(K);
     rv.store(V);
     if (wave == NW - 1) write_decays<C, false>(dec[0], rg, pr.scale);
   }
+  settle();
   __syncthreads();
   for (int t = 0, cur = 0; t < sp.n; t += C, cur ^= 1) {
     const bool more = t + C < sp.n;
-    if (more) fetch(t + C);
-    scores<TM, C, DX, NP, false>(Q, K, at.x16, P, dec[cur], pr.scale, wave, NW);
+    if (more) fetch_q(t + C);
+    scores<TM, C, DX, NP, false, NW>(Q, K, at.x16, P, dec[cur], pr.scale, wave);
+    if (more) fetch_k(t + C);
     f16v acc[C / 32];
     from_state<TM, C, DX, kPiecesX<TM>>(Q, at.x32, S, acc);
+    if (more) fetch_v(t + C);
     scale_rows<C>(acc, dec[cur].out);
     __syncthreads();
     within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(K, V, P, dec[cur], at, S, acc);

@@ -32,15 +32,14 @@ __device__ __forceinline__ float block_sum(float x, float* lds) {
 template <class TIn, class TM, int DX, int NW, bool DG>
 __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   constexpr int C = kChunk<TM>, DZ = NW * 32, NT = NW * 64, NP = kPiecesP<TM>;
-  constexpr int kScratch = NP * C * C > C * DZ ? NP * C * C : C * DZ;
-  __shared__ __align__(16) TM O[C * DX];
+  __shared__ __align__(16) TM O[C * (DX > DZ ? DX : DZ)];  // and then the chunk's dq
   __shared__ __align__(16) TM V[C * DX];
   __shared__ __align__(16) TM K[C * DZ];
-  __shared__ __align__(16) TM P[kScratch];  // q until the row sums are done, then the scores
-  __shared__ __align__(16) Decays<C> dec;
+  __shared__ __align__(16) TM P[NP * C * C];
+  __shared__ __align__(16) Decays<C> dec[2];
   __shared__ float part[NW][C];
   const LaProblem& pr = a.pr;
-  const int tid = threadIdx.x, wave = tid >> 6, z0 = wave * 32;
+  const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
   const Span sp = find_span(pr, slot);
   const int64_t row0 = (sp.batch * pr.T + sp.t0) * pr.H + h;  // of [B][T][H] arrays
@@ -66,44 +65,59 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   const TIn* qp = head_base<TIn>(a.q, sp.batch, sp.t0, h);
   const float* gp = gate_base(pr, sp.batch, sp.t0, h);
   TileRegs<TIn, C, DX, NT> ro, rv;
-  TileRegs<TIn, C, DZ, NT> rk, rq;
+  TileRegs<TIn, C, DZ, NT> rk;
   float rg = 0.f;
-  auto fetch = [&](int t) {
+  const auto fetch_o = [&](int t) {
     ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t);
-    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t);
-    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t);
-    if constexpr (DG) rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t);
-    if (wave == 0) rg = load_gate(gp, pr.gst, t, sp.n);
+    if (wave == NW - 1) rg = load_gate(gp, pr.gst, t, sp.n);
   };
-  fetch(0);
+  const auto fetch_v = [&](int t) { rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t); };
+  const auto fetch_k = [&](int t) { rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t); };
   const LaneOffsets<TM, C, DX, DZ> at(z0);
-  for (int t = 0; t < sp.n; t += C) {
-    ro.store(O);
-    rv.store(V);
-    rk.store(K);
-    if constexpr (DG) rq.store(P);
-    if (wave == 0) write_decays<C, false>(dec, rg, pr.scale);
-    __syncthreads();
-    if (t + C < sp.n) fetch(t + C);
+  fetch_o(0);
+  fetch_v(0);
+  fetch_k(0);
+  ro.store(O);
+  rv.store(V);
+  rk.store(K);
+  if (wave == NW - 1) write_decays<C, false>(dec[0], rg, pr.scale);
+  settle();
+  __syncthreads();
+  for (int t = 0, cur = 0; t < sp.n; t += C, cur ^= 1) {
+    const bool more = t + C < sp.n;
+    RowRegs<TIn, C> rq;
+    if constexpr (DG) rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t, z0);
+    scores<TM, C, DX, NP, false, NW>(O, V, at.x16, P, dec[cur], pr.scale, wave);
     f16v acc[C / 32];
     from_state<TM, C, DX, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(O, at.x32, S, acc);
-    scale_rows<C>(acc, dec.out);
-    if constexpr (DG) {
-      row_dots<TM, C, DZ>(acc, P, z0, part[wave]);
-      __syncthreads();
+    scale_rows<C>(acc, dec[cur].out);
+    if constexpr (DG) rq.dots(acc, part[wave]);
+    if (more) fetch_o(t + C);
+    __syncthreads();
+    if (more) fetch_v(t + C);
+    if constexpr (DG)
       if (tid < C && t + tid < sp.n) {
         float s = 0.f;
 #pragma unroll
         for (int w = 0; w < NW; ++w) s += part[w][tid];
         rows[row0 + (int64_t)(t + tid) * pr.H] = s;
       }
-    }
-    scores<TM, C, DX, NP, false>(O, V, at.x16, P, dec, pr.scale, wave, NW);
-    __syncthreads();
-    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(V, K, P, dec, at, S, acc);
+    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(V, K, P, dec[cur], at, S, acc);
+    if (more) fetch_k(t + C);
     const int64_t o = row0 * pr.Dk + (int64_t)t * ost;
+    OutRegs<TIn, C, DZ, NT> out;
     if (shared) store_rows<float, C>(acc, a.dq_part + o, ost, sp.n - t, pr.Dk, z0);
-    else store_rows<TIn, C>(acc, (TIn*)a.dq + o, ost, sp.n - t, pr.Dk, z0);
+    else rows_to_lds<TIn, C, DZ>(acc, (TIn*)O, z0);
+    if (more && wave == NW - 1) write_decays<C, false>(dec[cur ^ 1], rg, pr.scale);
+    __syncthreads();
+    if (!shared) out.take((const TIn*)O);
+    if constexpr (DX != DZ || sizeof(TIn) != sizeof(TM)) __syncthreads();
+    if (more) {
+      ro.store(O);
+      rv.store(V);
+      rk.store(K);
+    }
+    if (!shared) out.put((TIn*)a.dq + o, ost, sp.n - t, pr.Dk);
     __syncthreads();
   }
   if constexpr (DG) {  // <Lam, S> at the end of the span
@@ -127,15 +141,15 @@ template <class TIn, class TM, int D, bool DG>
 __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
   constexpr int C = kChunk<TM>, NW = D / 32, NT = NW * 128, NP = kPiecesP<TM>;
   __shared__ __align__(16) TM Q[C * D];
-  __shared__ __align__(16) TM K[C * D];
-  __shared__ __align__(16) TM V[C * D];
+  __shared__ __align__(16) TM K[C * D];  // and then the chunk's dk
+  __shared__ __align__(16) TM V[C * D];  // and then the chunk's dv
   __shared__ __align__(16) TM O[C * D];
   __shared__ __align__(16) TM P[2][NP * C * C];
-  __shared__ __align__(16) Decays<C> dec;
+  __shared__ __align__(16) Decays<C> dec[2];
   __shared__ float part[NW][C];
   __shared__ float sums[kTiles<C>][2][16];
   const LaProblem& pr = a.pr;
-  const int tid = threadIdx.x, wave = tid >> 6;
+  const int tid = threadIdx.x, wave = wave_id();
   const bool is_dk = wave >= NW;
   const int z0 = (is_dk ? wave - NW : wave) * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
@@ -171,32 +185,45 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
   const float* gp = gate_base(pr, sp.batch, sp.t0, h);
   TileRegs<TIn, C, D, NT> rq, rk, rv, ro;
   float rg = 0.f;
-  auto fetch = [&](int t) {
-    rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t);
+  const auto fetch_k = [&](int t) {
     rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t);
-    rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t);
-    ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t);
-    if (wave == 0) rg = load_gate(gp, pr.gst, t, sp.n);
+    if (wave == 2 * NW - 1) rg = load_gate(gp, pr.gst, t, sp.n);
   };
-  const int last = sp.n > 0 ? (sp.n - 1) / C * C : -C;
-  if (last >= 0) fetch(last);
-  const LaneOffsets<TM, C, D, D> at(z0);
-  for (int t = last; t >= 0; t -= C) {
+  const auto fetch_q = [&](int t) { rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t); };
+  const auto fetch_v = [&](int t) { rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t); };
+  const auto fetch_o = [&](int t) { ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t); };
+  const auto put_tiles = [&] {
     rq.store(Q);
     rk.store(K);
     rv.store(V);
     ro.store(O);
-    if (wave == 0) write_decays<C, true>(dec, rg, pr.scale);
-    __syncthreads();
-    if (t > 0) fetch(t - C);
+  };
+  const LaneOffsets<TM, C, D, D> at(z0);
+  const int last = sp.n > 0 ? (sp.n - 1) / C * C : -C;
+  if (last >= 0) {
+    fetch_k(last);
+    fetch_q(last);
+    fetch_v(last);
+    fetch_o(last);
+    put_tiles();
+    if (wave == 2 * NW - 1) write_decays<C, true>(dec[0], rg, pr.scale);
+  }
+  settle();
+  __syncthreads();
+  for (int t = last, cur = 0; t >= 0; t -= C, cur ^= 1) {
+    const bool more = t > 0;
+    if (more) fetch_k(t - C);
     {  // scores of both roles, and W's sums over i and over j
       const int l = fresh_lane();
       for (int i = wave; i < kTiles<C>; i += 2 * NW) {
         int rt, ct;
         tile_of<C, true>(i, rt, ct);
-        const f4v d = decay_tile<C, true>(dec, rt, ct, l);
-        f4v x = score_tile<TM, D>(K, Q, at.x16, rt, ct);
-        f4v y = score_tile<TM, D>(V, O, at.x16, rt, ct);
+        const f4v d = decay_tile<C, true>(dec[cur], rt, ct, l);
+        ScoreFrags<TM, D> fx, fy;
+        fx.read(K, Q, at.x16, rt, ct);
+        fy.read(V, O, at.x16, rt, ct);
+        step_fence();
+        f4v x = fx.product(), y = fy.product();
         float row[4], col = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -221,9 +248,11 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
         }
       }
     }
+    if (more) fetch_q(t - C);
     f16v acc[C / 32];
     from_state<TM, C, D, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(X, at.x32, S, acc);
-    scale_rows<C>(acc, dec.out);
+    scale_rows<C>(acc, dec[cur].out);
+    if (more) fetch_v(t - C);
     if constexpr (DG)
       if (is_dk) row_dots<TM, C, D>(acc, K, z0, part[wave - NW]);
     __syncthreads();
@@ -241,14 +270,24 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
         }
         rows[row0 + (int64_t)(t + tid) * pr.H] = s;
       }
-    within_chunk<TM, C, D, D, NP, kPiecesZ<TM>, true>(Y, Z, P[is_dk], dec, at, S, acc);
+    if (more) fetch_o(t - C);
+    within_chunk<TM, C, D, D, NP, kPiecesZ<TM>, true>(Y, Z, P[is_dk], dec[cur], at, S, acc);
+    const int64_t ok = row0 * pr.Dk + (int64_t)t * kst, ov = row0 * pr.Dv + (int64_t)t * vst;
     if (is_dk) {
-      const int64_t o = row0 * pr.Dk + (int64_t)t * kst;
-      if (shared) store_rows<float, C>(acc, a.dk_part + o, kst, sp.n - t, pr.Dk, z0);
-      else store_rows<TIn, C>(acc, (TIn*)a.dk + o, kst, sp.n - t, pr.Dk, z0);
+      if (shared) store_rows<float, C>(acc, a.dk_part + ok, kst, sp.n - t, pr.Dk, z0);
+      else rows_to_lds<TIn, C, D>(acc, (TIn*)K, z0);
     } else {
-      store_rows<TIn, C>(acc, (TIn*)a.dv + row0 * pr.Dv + (int64_t)t * vst, vst, sp.n - t, pr.Dv, z0);
+      rows_to_lds<TIn, C, D>(acc, (TIn*)V, z0);
     }
+    if (more && wave == 2 * NW - 1) write_decays<C, true>(dec[cur ^ 1], rg, pr.scale);
+    __syncthreads();
+    OutRegs<TIn, C, D, NT> outk, outv;
+    if (!shared) outk.take((const TIn*)K);
+    outv.take((const TIn*)V);
+    if constexpr (sizeof(TIn) != sizeof(TM)) __syncthreads();
+    if (more) put_tiles();
+    if (!shared) outk.put((TIn*)a.dk + ok, kst, sp.n - t, pr.Dk);
+    outv.put((TIn*)a.dv + ov, vst, sp.n - t, pr.Dv);
     __syncthreads();
   }
   if (sp.is_first && a.dh0 && !is_dk) store_state<D>(S, a.dh0 + outer, pr.Dv, 1, pr.Dk, pr.Dv, z0);

@@ -17,21 +17,21 @@ namespace la {
 template <class T>
 __device__ __forceinline__ f8v load8(const T* p) {
   if constexpr (sizeof(T) == 4) {
-    const f4v a = *(const f4v*)p, b = *(const f4v*)(p + 4);
+    const f4v a = __builtin_nontemporal_load((const f4v*)p), b = __builtin_nontemporal_load((const f4v*)(p + 4));
     return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
   } else {
     typedef T t8 __attribute__((ext_vector_type(8)));
-    return __builtin_convertvector(*(const t8*)p, f8v);
+    return __builtin_convertvector(__builtin_nontemporal_load((const t8*)p), f8v);
   }
 }
 template <class T>
 __device__ __forceinline__ void store8(T* p, f8v v) {
   if constexpr (sizeof(T) == 4) {
-    *(f4v*)p = __builtin_shufflevector(v, v, 0, 1, 2, 3);
-    *(f4v*)(p + 4) = __builtin_shufflevector(v, v, 4, 5, 6, 7);
+    __builtin_nontemporal_store(__builtin_shufflevector(v, v, 0, 1, 2, 3), (f4v*)p);
+    __builtin_nontemporal_store(__builtin_shufflevector(v, v, 4, 5, 6, 7), (f4v*)(p + 4));
   } else {
     typedef T t8 __attribute__((ext_vector_type(8)));
-    *(t8*)p = __builtin_convertvector(v, t8);
+    __builtin_nontemporal_store(__builtin_convertvector(v, t8), (t8*)p);
   }
 }
 __device__ __forceinline__ f8v load_weight(const void* w, int dtype, int at) {
@@ -85,8 +85,10 @@ __device__ __forceinline__ Angles load_angles(const NormProblem& p, int64_t b, i
   } else {
     const bool low = unit * 8 < half;
     const int at = low ? unit * 8 : unit * 8 - half;
-    a.c = load8<float>(p.cos + pos * half + at);
-    a.s = load8<float>(p.sin + pos * half + at);
+    const f4v* c = (const f4v*)(p.cos + pos * half + at);  // shared by the token's heads: not streamed
+    const f4v* s = (const f4v*)(p.sin + pos * half + at);
+    a.c = __builtin_shufflevector(c[0], c[1], 0, 1, 2, 3, 4, 5, 6, 7);
+    a.s = __builtin_shufflevector(s[0], s[1], 0, 1, 2, 3, 4, 5, 6, 7);
     if (low) a.s = -a.s;
   }
   return a;
