@@ -16,94 +16,98 @@ v [B, H, Dv], g [B, H] or [H], against state, fp32 [pool, H, Dk, Dv].
 from __future__ import annotations
 
 import contextlib
-import ctypes
+import struct
 
 import torch
 
-from . import MscanError, _check, _in_dtype, _ptr, _segments, _stream_handle, lib
+from . import _F16, _BF16, _F32, _check, _ptr, _segments, _stream_handle, lib
 
+# The C ABI's argument structs, packed by hand: building ctypes structures costs
+# several times as much, and a decoding step makes these calls for every layer.
+_ATTENTION = struct.Struct("@qqiiiiPif3q")        # mscan_attention
+_HEADS = struct.Struct("@P3q")                    # mscan_heads
+_NORM_ROPE = struct.Struct("@qqiiiiifPPqPiii4x")  # mscan_norm_rope
 
-class Attention(ctypes.Structure):
-    _fields_ = [
-        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("H", ctypes.c_int32), ("Hk", ctypes.c_int32),
-        ("Dk", ctypes.c_int32), ("Dv", ctypes.c_int32), ("cu_seqlens", ctypes.c_void_p), ("nseg", ctypes.c_int32),
-        ("scale", ctypes.c_float), ("g_strides", ctypes.c_int64 * 3),
-    ]
-
-
-class NormRope(ctypes.Structure):
-    _fields_ = [
-        ("B", ctypes.c_int64), ("T", ctypes.c_int64), ("Hq", ctypes.c_int32), ("Hk", ctypes.c_int32),
-        ("D", ctypes.c_int32), ("rot", ctypes.c_int32), ("interleaved", ctypes.c_int32), ("eps", ctypes.c_float),
-        ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p), ("table", ctypes.c_int64), ("positions", ctypes.c_void_p),
-        ("positions_int64", ctypes.c_int32), ("positions_per_batch", ctypes.c_int32), ("w_dtype", ctypes.c_int32),
-    ]
-
-
-class HeadsArray(ctypes.Structure):
-    _fields_ = [("p", ctypes.c_void_p), ("strides", ctypes.c_int64 * 3)]
+_DTYPES = {torch.float32: _F32, torch.bfloat16: _BF16, torch.float16: _F16}
+_HERE = contextlib.nullcontext()
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
 def _on(device):
     """Make the tensors' device the current one for a call's launches."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(device)
+    return _HERE if device.index == _current_device() else torch.cuda.device(device)
 
 
-def _same_device(dev, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, the queries on {dev}")
+def _dtype(t, name):
+    d = _DTYPES.get(t.dtype)
+    if d is None:
+        raise ValueError(f"{name}: only float32, bfloat16 and float16 are supported")
+    return d
 
 
-def _heads(t, name):
-    if t.stride(3) != 1 and t.shape[3] != 1:
-        raise ValueError(f"{name}: the last axis must be contiguous")
-    unit = 16 // t.element_size()
-    # the stride of an axis of one entry is never used
-    st = [0 if t.shape[i] == 1 else t.stride(i) for i in range(3)]
-    if t.data_ptr() % 16 or st[0] % unit or st[1] % unit or st[2] % unit:
-        raise ValueError(f"{name}: rows must be 16-byte aligned (a storage offset and strides of whole 16 bytes)")
-    return HeadsArray(t.data_ptr(), (ctypes.c_int64 * 3)(*st))
+def _other_device(dev, name, t):
+    raise ValueError(f"{name} is on {t.device}, the queries on {dev}")
 
 
-def _attention(q, k, v, g, cu_seqlens, scale):
-    """(problem, dtype, cu_seqlens, number of sequences) of a call, checked."""
-    if not q.is_cuda:
-        raise ValueError("q must be a GPU tensor")
-    dev = q.device
-    if q.dim() != 4 or v.dim() != 4 or k.shape != q.shape or v.shape[:2] != q.shape[:2]:
-        raise ValueError("q and k must be [B, T, Hk, Dk] and v [B, T, H, Dv]")
-    if k.dtype != q.dtype or v.dtype != q.dtype:
-        raise ValueError("q, k and v must have the same dtype")
-    dt = _in_dtype(q, "q")
-    B, T, Hk, Dk = (int(x) for x in q.shape)
-    H, Dv = int(v.shape[2]), int(v.shape[3])
+def _heads(t, name, strides=None):
+    """mscan_heads of a [B, T, heads, d] tensor (or of one with these strides)."""
+    s0, s1, s2, s3 = t.stride() if strides is None else strides
+    p, unit = t.data_ptr(), 16 // t.element_size()
+    if s3 != 1 or p % 16 or s0 % unit or s1 % unit or s2 % unit:
+        # the stride of an axis of one entry is never used
+        b, n, h, d = t.shape if strides is None else (t.shape[0], 1, *t.shape[1:])
+        s0, s1, s2 = s0 if b > 1 else 0, s1 if n > 1 else 0, s2 if h > 1 else 0
+        if s3 != 1 and d != 1:
+            raise ValueError(f"{name}: the last axis must be contiguous")
+        if p % 16 or s0 % unit or s1 % unit or s2 % unit:
+            raise ValueError(f"{name}: rows must be 16-byte aligned (a storage offset and strides of whole 16 bytes)")
+    return _HEADS.pack(p, s0, s1, s2)
+
+
+def _check_sizes(H, Hk, Dk, Dv):
     if Hk == 0 or H == 0 or H % Hk:
         raise ValueError(f"the number of value heads ({H}) must be a multiple of the number of key heads ({Hk})")
     for d, n in ((Dk, "Dk"), (Dv, "Dv")):
         if d % 8 or not 8 <= d <= 128:
             raise ValueError(f"{n} must be a multiple of 8 up to 128, got {d}")
+
+
+def _attention(q, k, v, g, cu_seqlens, scale):
+    """(mscan_attention, dtype, shape of the states, whether there is anything to
+    run) of a call on whole sequences, checked. Keep cu_seqlens alive."""
+    if not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
+    dev, shape, vshape = q.device, q.shape, v.shape
+    if len(shape) != 4 or len(vshape) != 4 or k.shape != shape or vshape[:2] != shape[:2]:
+        raise ValueError("q and k must be [B, T, Hk, Dk] and v [B, T, H, Dv]")
+    dt = _dtype(q, "q")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have the same dtype")
+    B, T, Hk, Dk = shape
+    H, Dv = vshape[2], vshape[3]
+    if H % (Hk or H + 1) or H == 0 or (Dk | Dv) % 8 or not 0 < Dk <= 128 or not 0 < Dv <= 128:
+        _check_sizes(H, Hk, Dk, Dv)
     if g.dtype != torch.float32:
         raise ValueError("g (log decays) must be float32")
-    if tuple(g.shape) == (H,):
-        gs = (0, 0, g.stride(0))
-    elif tuple(g.shape) == (B, T, H):
-        gs = g.stride()
+    if g.shape == (B, T, H):
+        g0, g1, g2 = g.stride()
+    elif g.shape == (H,):
+        g0, g1, g2 = 0, 0, g.stride(0)
     else:
         raise ValueError(f"g must be [B, T, H] = {(B, T, H)} or [H], got {tuple(g.shape)}")
-    _same_device(dev, k=k, v=v, g=g)
-    cu, nseg = _segments(cu_seqlens, dev, T)
-    if cu is None:
-        nseg = B
-    elif B != 1:
-        raise ValueError("cu_seqlens needs B = 1 (packed sequences)")
-    else:
-        _same_device(dev, cu_seqlens=cu)
-    prob = Attention(B, T, H, Hk, Dk, Dv, None if cu is None else cu.data_ptr(), nseg,
-                     float(Dk ** -0.5 if scale is None else scale), (ctypes.c_int64 * 3)(*gs))
-    return prob, dt, cu, nseg
+    for t, name in ((k, "k"), (v, "v"), (g, "g")):
+        if t.device != dev:
+            _other_device(dev, name, t)
+    n, cu = B, None
+    if cu_seqlens is not None:
+        cu, n = _segments(cu_seqlens, dev, T)
+        if B != 1:
+            raise ValueError("cu_seqlens needs B = 1 (packed sequences)")
+        if cu.device != dev:
+            _other_device(dev, "cu_seqlens", cu)
+    prob = _ATTENTION.pack(B, T, H, Hk, Dk, Dv, 0 if cu is None else cu.data_ptr(), n,
+                           Dk ** -0.5 if scale is None else scale, g0, g1, g2)
+    return prob, dt, (n, H, Dk, Dv), B * T * n > 0, cu
 
 
 def _states(t, shape, name, dev):
@@ -111,7 +115,7 @@ def _states(t, shape, name, dev):
         return None
     if t.dtype != torch.float32 or t.device != dev or not t.is_contiguous() or t.data_ptr() % 16:
         raise ValueError(f"{name} must be a contiguous, 16-byte aligned fp32 tensor on {dev}")
-    if tuple(t.shape) != shape:
+    if t.shape != shape:
         raise ValueError(f"{name} must be [N, H, Dk, Dv] = {shape}, got {tuple(t.shape)}")
     return t
 
@@ -119,7 +123,7 @@ def _states(t, shape, name, dev):
 def _space(prob, backward, dev):
     """A workspace of the call's own: torch's allocator keeps it in the stream's
     order, and in a captured graph's own pool."""
-    need = lib.linear_attention_workspace_bytes(ctypes.byref(prob), backward)
+    need = lib.linear_attention_workspace_bytes(prob, backward)
     if need <= 256:
         return None, 0
     return torch.empty(need, dtype=torch.uint8, device=dev), need
@@ -128,22 +132,20 @@ def _space(prob, backward, dev):
 def linear_attention_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=None, need_ht=True):
     """S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t: (o, ht), ht the
     state after each sequence (None without need_ht)."""
-    prob, dt, cu, nseg = _attention(q, k, v, g, cu_seqlens, scale)
+    prob, dt, shape, work, cu = _attention(q, k, v, g, cu_seqlens, scale)
     dev = q.device
-    shape = (nseg, prob.H, prob.Dk, prob.Dv)
     h0 = _states(h0, shape, "h0", dev)
     qh, kh, vh = _heads(q, "q"), _heads(k, "k"), _heads(v, "v")
     o = torch.empty(v.shape, dtype=v.dtype, device=dev)
     ht = torch.empty(shape, dtype=torch.float32, device=dev) if need_ht else None
-    if prob.B == 0 or prob.T == 0 or nseg == 0:
+    if not work:
         if need_ht:
             ht.zero_() if h0 is None else ht.copy_(h0)
         return o, ht
     with _on(dev):
         ws, n = _space(prob, 0, dev)
         _check("linear_attention_fwd", lib.linear_attention_fwd(
-            ctypes.byref(prob), dt, ctypes.byref(qh), ctypes.byref(kh), ctypes.byref(vh), _ptr(g), _ptr(h0), _ptr(o),
-            _ptr(ht), _ptr(ws), n, _stream_handle(dev)))
+            prob, dt, qh, kh, vh, g.data_ptr(), _ptr(h0), o.data_ptr(), _ptr(ht), _ptr(ws), n, _stream_handle(dev)))
     return o, ht
 
 
@@ -151,9 +153,8 @@ def linear_attention_bwd(q, k, v, g, do, h0=None, dht=None, cu_seqlens=None, sca
     """Adjoint of linear_attention_fwd for the gradients do of o and dht of ht
     (None: zero): (dq, dk, dv, dg, dh0), dg of g's shape and dh0 in fp32 (None
     when not needed)."""
-    prob, dt, cu, nseg = _attention(q, k, v, g, cu_seqlens, scale)
+    prob, dt, shape, work, cu = _attention(q, k, v, g, cu_seqlens, scale)
     dev = q.device
-    shape = (nseg, prob.H, prob.Dk, prob.Dv)
     h0, dht = _states(h0, shape, "h0", dev), _states(dht, shape, "dht", dev)
     if do.shape != v.shape or do.dtype != v.dtype or do.device != dev:
         raise ValueError("do must have the shape, dtype and device of v")
@@ -161,7 +162,7 @@ def linear_attention_bwd(q, k, v, g, do, h0=None, dht=None, cu_seqlens=None, sca
     dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=dev) for x in (q, k, v))
     dg = torch.empty(g.shape, dtype=torch.float32, device=dev) if need_dg else None
     dh0 = torch.empty(shape, dtype=torch.float32, device=dev) if need_dh0 else None
-    if prob.B == 0 or prob.T == 0 or nseg == 0:
+    if not work:
         if need_dg:
             dg.zero_()
         if need_dh0:
@@ -170,9 +171,8 @@ def linear_attention_bwd(q, k, v, g, do, h0=None, dht=None, cu_seqlens=None, sca
     with _on(dev):
         ws, n = _space(prob, 1, dev)
         _check("linear_attention_bwd", lib.linear_attention_bwd(
-            ctypes.byref(prob), dt, ctypes.byref(qh), ctypes.byref(kh), ctypes.byref(vh), _ptr(g), ctypes.byref(oh),
-            _ptr(h0), _ptr(dht), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg), int(g.dim() == 1), _ptr(dh0), _ptr(ws), n,
-            _stream_handle(dev)))
+            prob, dt, qh, kh, vh, g.data_ptr(), oh, _ptr(h0), _ptr(dht), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
+            int(g.dim() == 1), _ptr(dh0), _ptr(ws), n, _stream_handle(dev)))
     return dq, dk, dv, dg, dh0
 
 
@@ -183,78 +183,118 @@ def linear_attention_step(q, k, v, g, state, slots=None, scale=None):
     slots: int32 [B] on the GPU, or None (row b has state b). A slot outside
     [0, pool) marks a row of padding, with an output of zero. Rows that share a
     slot are consecutive steps of that sequence, in the order of the batch."""
-    if q.dim() != 3 or k.dim() != 3 or v.dim() != 3 or g.dim() not in (1, 2):
-        raise ValueError("q and k must be [B, Hk, Dk], v [B, H, Dv] and g [B, H] or [H]")
-    prob, dt, _, _ = _attention(q[:, None], k[:, None], v[:, None], g[:, None] if g.dim() == 2 else g, None, scale)
-    dev, B = q.device, prob.B
-    if state.dim() != 4 or tuple(state.shape[1:]) != (prob.H, prob.Dk, prob.Dv):
-        raise ValueError(f"state must be [pool, H, Dk, Dv] with {(prob.H, prob.Dk, prob.Dv)}, got {tuple(state.shape)}")
-    pool = int(state.shape[0])
-    _states(state, tuple(state.shape), "state", dev)
+    shape, vshape, dev = q.shape, v.shape, q.device
+    if not q.is_cuda:
+        raise ValueError("q must be a GPU tensor")
+    if len(shape) != 3 or k.shape != shape or len(vshape) != 3 or vshape[0] != shape[0]:
+        raise ValueError("q and k must be [B, Hk, Dk] and v [B, H, Dv]")
+    dt = _dtype(q, "q")
+    if k.dtype != q.dtype or v.dtype != q.dtype:
+        raise ValueError("q, k and v must have the same dtype")
+    B, Hk, Dk = shape
+    H, Dv = vshape[1], vshape[2]
+    if H % (Hk or H + 1) or H == 0 or (Dk | Dv) % 8 or not 0 < Dk <= 128 or not 0 < Dv <= 128:
+        _check_sizes(H, Hk, Dk, Dv)
+    if g.dtype != torch.float32:
+        raise ValueError("g (log decays) must be float32")
+    if g.shape == (B, H):
+        g0, g2 = g.stride()
+    elif g.shape == (H,):
+        g0, g2 = 0, g.stride(0)
+    else:
+        raise ValueError(f"g must be [B, H] = {(B, H)} or [H], got {tuple(g.shape)}")
+    pool = state.shape[0] if state.dim() == 4 else 0
+    if state.shape != (pool, H, Dk, Dv):
+        raise ValueError(f"state must be [pool, H, Dk, Dv] with {(H, Dk, Dv)}, got {tuple(state.shape)}")
+    if state.dtype != torch.float32 or not state.is_contiguous() or state.data_ptr() % 16:
+        raise ValueError("state must be a contiguous, 16-byte aligned fp32 tensor")
     if slots is None:
         if B > pool:
             raise ValueError(f"{B} rows without slots need as many states, got {pool}")
-    elif slots.dtype != torch.int32 or slots.device != dev or tuple(slots.shape) != (B,) or not slots.is_contiguous():
+    elif slots.dtype != torch.int32 or slots.device != dev or slots.shape != (B,) or not slots.is_contiguous():
         raise ValueError(f"slots must be a contiguous int32 tensor [B] on {dev}")
-    qh, kh, vh = _heads(q[:, None], "q"), _heads(k[:, None], "k"), _heads(v[:, None], "v")
-    o = torch.empty(v.shape, dtype=v.dtype, device=dev)
+    for t, name in ((k, "k"), (v, "v"), (g, "g"), (state, "state")):
+        if t.device != dev:
+            _other_device(dev, name, t)
+
+    def heads(t, name):
+        s0, s1, s2 = t.stride()
+        return _heads(t, name, (s0, 0, s1, s2))
+
+    o = torch.empty(vshape, dtype=v.dtype, device=dev)
     if B == 0:
         return o
     if pool == 0:
         return o.zero_()  # every row is padding
+    prob = _ATTENTION.pack(B, 1, H, Hk, Dk, Dv, 0, B, Dk ** -0.5 if scale is None else scale, g0, 0, g2)
     with _on(dev):
         _check("linear_attention_step", lib.linear_attention_step(
-            ctypes.byref(prob), dt, ctypes.byref(qh), ctypes.byref(kh), ctypes.byref(vh), _ptr(g), _ptr(slots), pool,
-            _ptr(state), _ptr(o), _stream_handle(dev)))
+            prob, dt, heads(q, "q"), heads(k, "k"), heads(v, "v"), g.data_ptr(), _ptr(slots), pool, state.data_ptr(),
+            o.data_ptr(), _stream_handle(dev)))
     return o
 
 
 def _norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
-    """(problem, dtype) of a norm call, checked."""
+    """(mscan_norm_rope, dtype, whether there is anything to run) of a call, checked."""
     if not q.is_cuda:
         raise ValueError("q must be a GPU tensor")
-    dev = q.device
-    if q.dim() != 4 or k.dim() != 4 or q.shape[:2] != k.shape[:2] or q.shape[3] != k.shape[3]:
+    dev, shape, kshape = q.device, q.shape, k.shape
+    if len(shape) != 4 or len(kshape) != 4 or shape[:2] != kshape[:2] or shape[3] != kshape[3]:
         raise ValueError("q must be [B, T, Hq, D] and k [B, T, Hk, D]")
+    dt = _dtype(q, "q")
     if k.dtype != q.dtype:
         raise ValueError("q and k must have the same dtype")
-    dt = _in_dtype(q, "q")
-    B, T, Hq, D = (int(x) for x in q.shape)
-    Hk = int(k.shape[2])
+    B, T, Hq, D = shape
+    Hk = kshape[2]
+    if Hq == 0 or Hk == 0:
+        raise ValueError("q and k both need heads")
     if D % 8 or not 8 <= D <= 256:
         raise ValueError(f"the head size must be a multiple of 8 up to 256, got {D}")
+    if not eps >= 0:
+        raise ValueError(f"eps must not be negative, got {eps}")
     wt = 0
-    if (q_weight is None) != (k_weight is None):
-        raise ValueError("give both weights or neither")
-    if q_weight is not None:
-        if q_weight.dtype != k_weight.dtype:
+    if q_weight is not None and k_weight is not None:
+        wt = _dtype(q_weight, "q_weight")
+        if k_weight.dtype != q_weight.dtype:
             raise ValueError("q_weight and k_weight must have the same dtype")
-        wt = _in_dtype(q_weight, "q_weight")
         for w, n in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-            if tuple(w.shape) != (D,) or not w.is_contiguous():
+            if w.shape != (D,) or not w.is_contiguous():
                 raise ValueError(f"{n} must be a contiguous tensor [D] = {(D,)}, got {tuple(w.shape)}")
-    rot, table = 0, 0
-    if (cos is None) != (sin is None):
-        raise ValueError("give both cos and sin or neither")
-    if cos is not None:
+            if w.device != dev:
+                _other_device(dev, n, w)
+    elif q_weight is not None or k_weight is not None:
+        raise ValueError("give both weights or neither")
+    rot, table, cp, sp = 0, 0, 0, 0
+    if cos is not None and sin is not None:
         for x, n in ((cos, "cos"), (sin, "sin")):
             if x.dtype != torch.float32 or x.dim() != 2 or not x.is_contiguous() or x.data_ptr() % 16:
                 raise ValueError(f"{n} must be a contiguous, 16-byte aligned fp32 tensor [positions, rot / 2]")
-        if cos.shape != sin.shape or cos.shape[0] < 1:
+            if x.device != dev:
+                _other_device(dev, n, x)
+        table, rot = cos.shape
+        if sin.shape != (table, rot) or table < 1:
             raise ValueError("cos and sin must have one shape, with at least one position")
-        table, rot = int(cos.shape[0]), 2 * int(cos.shape[1])
+        rot *= 2
         if rot % 16 or rot > D:
             raise ValueError(f"the rotated entries must be a multiple of 16 up to the head size, got {rot}")
-    per_batch = i64 = 0
+        cp, sp = cos.data_ptr(), sin.data_ptr()
+    elif cos is not None or sin is not None:
+        raise ValueError("give both cos and sin or neither")
+    per_batch = i64 = pp = 0
     if positions is not None:
-        if positions.dtype not in (torch.int32, torch.int64) or not positions.is_contiguous():
+        i64 = positions.dtype == torch.int64
+        if not (i64 or positions.dtype == torch.int32) or not positions.is_contiguous():
             raise ValueError("positions must be a contiguous int32 or int64 tensor")
-        if tuple(positions.shape) not in ((T,), (B, T)):
+        per_batch = positions.dim() == 2
+        if positions.shape != ((B, T) if per_batch else (T,)):
             raise ValueError(f"positions must be [T] or [B, T], got {tuple(positions.shape)}")
-        per_batch, i64 = int(positions.dim() == 2), int(positions.dtype == torch.int64)
-    _same_device(dev, k=k, q_weight=q_weight, k_weight=k_weight, cos=cos, sin=sin, positions=positions)
-    return NormRope(B, T, Hq, Hk, D, rot, int(bool(interleaved)), float(eps), _ptr(cos), _ptr(sin), table,
-                    _ptr(positions), i64, per_batch, wt), dt
+        if positions.device != dev:
+            _other_device(dev, "positions", positions)
+        pp = positions.data_ptr()
+    if k.device != dev:
+        _other_device(dev, "k", k)
+    return _NORM_ROPE.pack(B, T, Hq, Hk, D, rot, bool(interleaved), eps, cp, sp, table, pp, i64, per_batch,
+                           wt), dt, B * T > 0
 
 
 def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6,
@@ -265,18 +305,14 @@ def qk_norm_rope_fwd(q, k, q_weight=None, k_weight=None, cos=None, sin=None, pos
     (positions: [T] or [B, T], default 0, 1, ..). Pairs are entries (i, i + rot /
     2), or (2i, 2i + 1) when interleaved. No weights: ones; no cos, sin: no
     rotation."""
-    prob, dt = _norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    prob, dt, work = _norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     dev = q.device
     qh, kh = _heads(q, "q"), _heads(k, "k")
     yq, yk = torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(k.shape, dtype=k.dtype, device=dev)
-    if prob.B * prob.T * prob.Hq * prob.Hk == 0:
-        if q.numel() or k.numel():
-            raise ValueError("q and k both need heads")
-        return yq, yk
-    with _on(dev):
-        _check("qk_norm_rope_fwd", lib.qk_norm_rope_fwd(
-            ctypes.byref(prob), dt, ctypes.byref(qh), ctypes.byref(kh), _ptr(q_weight), _ptr(k_weight), _ptr(yq),
-            _ptr(yk), _stream_handle(dev)))
+    if work:
+        with _on(dev):
+            _check("qk_norm_rope_fwd", lib.qk_norm_rope_fwd(
+                prob, dt, qh, kh, _ptr(q_weight), _ptr(k_weight), yq.data_ptr(), yk.data_ptr(), _stream_handle(dev)))
     return yq, yk
 
 
@@ -284,7 +320,7 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, dyq, dyk, positions=Non
                      need_dw=True):
     """Adjoint of qk_norm_rope_fwd: (dq, dk, dq_weight, dk_weight), the weights'
     gradients in fp32 (None without weights or need_dw)."""
-    prob, dt = _norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    prob, dt, work = _norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
     dev = q.device
     for x, d, n in ((q, dyq, "dyq"), (k, dyk, "dyk")):
         if d.shape != x.shape or d.dtype != x.dtype or d.device != dev:
@@ -293,17 +329,14 @@ def qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, dyq, dyk, positions=Non
     dq, dk = torch.empty(q.shape, dtype=q.dtype, device=dev), torch.empty(k.shape, dtype=k.dtype, device=dev)
     dwq = dwk = None
     if q_weight is not None and need_dw:
-        dwq = torch.empty(prob.D, dtype=torch.float32, device=dev)
-        dwk = torch.empty(prob.D, dtype=torch.float32, device=dev)
-    if prob.B * prob.T * prob.Hq * prob.Hk == 0:
-        if q.numel() or k.numel():
-            raise ValueError("q and k both need heads")
+        dwq = torch.empty(q.shape[3], dtype=torch.float32, device=dev)
+        dwk = torch.empty(q.shape[3], dtype=torch.float32, device=dev)
+    if not work:
         return dq, dk, (None if dwq is None else dwq.zero_()), (None if dwk is None else dwk.zero_())
     with _on(dev):
-        need = lib.qk_norm_rope_workspace_bytes(ctypes.byref(prob))
+        need = lib.qk_norm_rope_workspace_bytes(prob)
         ws = torch.empty(need, dtype=torch.uint8, device=dev)
         _check("qk_norm_rope_bwd", lib.qk_norm_rope_bwd(
-            ctypes.byref(prob), dt, ctypes.byref(qh), ctypes.byref(kh), _ptr(q_weight), _ptr(k_weight),
-            ctypes.byref(dqh), ctypes.byref(dkh), _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk), _ptr(ws), need,
-            _stream_handle(dev)))
+            prob, dt, qh, kh, _ptr(q_weight), _ptr(k_weight), dqh, dkh, _ptr(dq), _ptr(dk), _ptr(dwq), _ptr(dwk),
+            _ptr(ws), need, _stream_handle(dev)))
     return dq, dk, dwq, dwk

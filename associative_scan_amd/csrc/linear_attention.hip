@@ -148,24 +148,35 @@ hipError_t launch_join(const LaProblem& p, bool rev, const float* outer, float* 
 }
 
 // Steps per span. A workgroup per head and sequence needs no second pass over
-// k and v, but fills the card only with many heads and sequences; with fewer, the
-// rows are cut so that the workgroups fill the card's 512 places (two on each of
-// 256 CUs) a whole number of times, as far as spans of 256 steps allow.
+// k and v, but fills the card only with many heads and sequences; with fewer the
+// time axis is cut. What a cut costs, in steps of the main pass (64 of them take
+// about 5 us on a CU of their own, 8 us where two workgroups share one): its spans
+// one after the other in as many rounds as the card's 512 places ask for, 0.45 of
+// that for the pass that gives the spans' own states, a round's start, and about
+// two chunks for the join and the launches.
 void plan(LaProblem& p, bool backward) {
-  const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H, places = 512;
-  int64_t best = p.T, best_cost = INT64_MAX;
-  for (int64_t r = 1; r <= 4; ++r) {
-    const int64_t n = places * r / rows;  // spans per row that fill r rounds
-    if (n < 1) continue;
-    int64_t span = ((p.T + n - 1) / n + 63) / 64 * 64;
-    if (span < 256) span = 256;
-    const int64_t blocks = (p.T + span - 1) / span * rows;
-    const int64_t cost = (blocks + places - 1) / places * (span + 64);  // and a chunk's time to start up
-    if (cost < best_cost) {
-      best_cost = cost;
+  const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H;
+  const auto cost = [&](int64_t span) {
+    const int64_t n = (p.T + span - 1) / span, blocks = n * rows;
+    const int64_t rounds = (blocks + 511) / 512;
+    const double step = blocks <= 256 ? 0.62 : 1.0;
+    const double run = rounds * step * ((double)(span < p.T ? span : p.T) + 48);
+    return n == 1 ? run : 1.45 * run + 128 + 3.0 * n;
+  };
+  int64_t best = (p.T + 63) / 64 * 64;
+  double least = cost(best);
+  const auto offer = [&](int64_t span) {
+    span = (span + 63) / 64 * 64;
+    if (span < 64 || span >= p.T) return;
+    const double c = cost(span);
+    if (c < least) {
+      least = c;
       best = span;
     }
-  }
+  };
+  for (int64_t blocks = 256; blocks <= 4096; blocks += 256)
+    if (blocks >= rows) offer((p.T + blocks / rows - 1) / (blocks / rows));
+  for (int64_t span = 64; span <= 1024; span *= 2) offer(span);
   p.span = best;
   if (p.cu) {
     p.spans = 0;
