@@ -62,7 +62,7 @@ __global__ __launch_bounds__(256) void k_attn_step(const StepArgs a) {
   for (int i = 0; i < N; ++i) {
     const int row = r0 + i * RW;
     S[i] = f4v{0.f, 0.f, 0.f, 0.f};
-    if (live && in && row < a.Dk) S[i] = *(const f4v*)(sp + (int64_t)row * a.Dv);
+    if (live && in && row < a.Dk) S[i] = __builtin_nontemporal_load((const f4v*)(sp + (int64_t)row * a.Dv));
   }
   // the loads above are in flight; what is read of a state another row owns is dropped
   if (a.slots && live && slot_taken_before(a.slots, b0, slot)) return;
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(256) void k_attn_step(const StepArgs a) {
 #pragma unroll
   for (int i = 0; i < N; ++i) {
     const int row = r0 + i * RW;
-    if (in && row < a.Dk) *(f4v*)(sp + (int64_t)row * a.Dv) = S[i];
+    if (in && row < a.Dk) __builtin_nontemporal_store(S[i], (f4v*)(sp + (int64_t)row * a.Dv));
   }
 }
 

@@ -5,9 +5,11 @@
 //
 // Every element is read once and written once: the kernels are bound by HBM. A
 // row (one head of one token) is spread over L = 8, 16 or 32 lanes of 8 elements,
-// so a wave reads whole rows as 16-byte units; the pair of an element lies in
-// another lane's unit (or, interleaved, in its own). A lane group takes several
-// heads of a token and reads the token's angles once.
+// two units of 4. A rotated lane holds both halves of its four pairs, (4 c + i,
+// rot / 2 + 4 c + i), so the rotation needs nothing from other lanes and a pair
+// shares its angle; 16 lanes still read 128 contiguous bytes at a time. A lane
+// group takes several heads of a token and reads the token's angles once. Loads
+// and stores are streaming: they pass the caches by for inputs that come back.
 #include "la_device.hpp"
 #include "qk_norm_rope.hpp"
 
@@ -15,95 +17,91 @@ namespace mscan {
 namespace la {
 
 template <class T>
-__device__ __forceinline__ f8v load8(const T* p) {
-  if constexpr (sizeof(T) == 4) {
-    const f4v a = __builtin_nontemporal_load((const f4v*)p), b = __builtin_nontemporal_load((const f4v*)(p + 4));
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  } else {
-    typedef T t8 __attribute__((ext_vector_type(8)));
-    return __builtin_convertvector(__builtin_nontemporal_load((const t8*)p), f8v);
-  }
+__device__ __forceinline__ f4v load4(const T* p) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  return __builtin_convertvector(__builtin_nontemporal_load((const t4*)p), f4v);
 }
 template <class T>
-__device__ __forceinline__ void store8(T* p, f8v v) {
-  if constexpr (sizeof(T) == 4) {
-    __builtin_nontemporal_store(__builtin_shufflevector(v, v, 0, 1, 2, 3), (f4v*)p);
-    __builtin_nontemporal_store(__builtin_shufflevector(v, v, 4, 5, 6, 7), (f4v*)(p + 4));
-  } else {
-    typedef T t8 __attribute__((ext_vector_type(8)));
-    __builtin_nontemporal_store(__builtin_convertvector(v, t8), (t8*)p);
-  }
+__device__ __forceinline__ void store4(T* p, f4v v) {
+  typedef T t4 __attribute__((ext_vector_type(4)));
+  __builtin_nontemporal_store(__builtin_convertvector(v, t4), (t4*)p);
 }
-__device__ __forceinline__ f8v load_weight(const void* w, int dtype, int at) {
-  f8v v = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+__device__ __forceinline__ f4v load_weight(const void* w, int dtype, int at) {
+  f4v v = {1.f, 1.f, 1.f, 1.f};
   if (!w) return v;
 #pragma unroll
-  for (int i = 0; i < 8; ++i)
+  for (int i = 0; i < 4; ++i)
     v[i] = dtype == 0 ? ((const float*)w)[at + i]
                       : dtype == 1 ? (float)((const __bf16*)w)[at + i] : (float)((const _Float16*)w)[at + i];
   return v;
 }
 
-// sum over the L lanes of a row
+template <int CTRL>
+__device__ __forceinline__ float dpp_plus(float x) {
+  return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, false));
+}
+// sum over the L lanes of a row, to all of them
 template <int L>
 __device__ __forceinline__ float row_sum(float x) {
-#pragma unroll
-  for (int m = 1; m < L; m <<= 1) x += __shfl_xor(x, m);
+  x = dpp_plus<0xb1>(x);   // quad_perm 1,0,3,2
+  x = dpp_plus<0x4e>(x);   // quad_perm 2,3,0,1
+  x = dpp_plus<0x141>(x);  // row_half_mirror: the other quad of 8
+  if constexpr (L >= 16) x = dpp_plus<0x140>(x);  // row_mirror: the other half of 16
+  if constexpr (L >= 32) {
+    const uint32_t w = __builtin_bit_cast(uint32_t, x);
+    const auto y = __builtin_amdgcn_permlane16_swap(w, w, false, false);
+    x = __builtin_bit_cast(float, (uint32_t)y[0]) + __builtin_bit_cast(float, (uint32_t)y[1]);
+  }
   return x;
 }
-__device__ __forceinline__ float dot8(f8v a, f8v b) {
-  return ((a[0] * b[0] + a[1] * b[1]) + (a[2] * b[2] + a[3] * b[3])) +
-         ((a[4] * b[4] + a[5] * b[5]) + (a[6] * b[6] + a[7] * b[7]));
-}
+__device__ __forceinline__ float dot4(f4v a, f4v b) { return (a[0] * b[0] + a[1] * b[1]) + (a[2] * b[2] + a[3] * b[3]); }
 
-// The angles that a lane's 8 elements need: c[i], and s[i] with the sign that
-// its pair's value enters with (the transposed rotation flips it).
-struct Angles {
-  f8v c, s;
+// A lane's two units of a row, and the angles of its pairs (1 and 0 where it has
+// none). Interleaved pairs lie inside a unit.
+struct Place {
+  int a, b;
+  bool in, rotated;
 };
 template <bool PAIRS>
-__device__ __forceinline__ Angles load_angles(const NormProblem& p, int64_t b, int64_t t, int unit) {
-  Angles a;
-  a.c = f8v{1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-  a.s = f8v{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  if (unit * 8 >= p.rot) return a;
+__device__ __forceinline__ Place place_of(const NormProblem& p, int lane) {
+  Place q;
+  q.in = lane * 8 < p.D;
+  q.rotated = lane * 8 < p.rot;
+  q.a = q.rotated && !PAIRS ? lane * 4 : lane * 8;
+  q.b = q.rotated && !PAIRS ? p.rot / 2 + lane * 4 : lane * 8 + 4;
+  return q;
+}
+struct Angles {
+  f4v c, s;
+};
+__device__ __forceinline__ Angles load_angles(const NormProblem& p, int64_t b, int64_t t, int lane) {
   int64_t pos = t;
   if (p.positions) {
     const int64_t at = p.per_batch ? b * p.T + t : t;
     pos = p.positions64 ? ((const int64_t*)p.positions)[at] : (int64_t)((const int32_t*)p.positions)[at];
   }
   pos = pos < 0 ? 0 : (pos >= p.table ? p.table - 1 : pos);
-  const int half = p.rot / 2;
-  if constexpr (PAIRS) {
-    const f4v c = *(const f4v*)(p.cos + pos * half + unit * 4), s = *(const f4v*)(p.sin + pos * half + unit * 4);
-    a.c = __builtin_shufflevector(c, c, 0, 0, 1, 1, 2, 2, 3, 3);
-    a.s = __builtin_shufflevector(s, s, 0, 0, 1, 1, 2, 2, 3, 3);
-    a.s[0] = -a.s[0];
-    a.s[2] = -a.s[2];
-    a.s[4] = -a.s[4];
-    a.s[6] = -a.s[6];
-  } else {
-    const bool low = unit * 8 < half;
-    const int at = low ? unit * 8 : unit * 8 - half;
-    const f4v* c = (const f4v*)(p.cos + pos * half + at);  // shared by the token's heads: not streamed
-    const f4v* s = (const f4v*)(p.sin + pos * half + at);
-    a.c = __builtin_shufflevector(c[0], c[1], 0, 1, 2, 3, 4, 5, 6, 7);
-    a.s = __builtin_shufflevector(s[0], s[1], 0, 1, 2, 3, 4, 5, 6, 7);
-    if (low) a.s = -a.s;
-  }
-  return a;
+  const int64_t at = pos * (p.rot / 2) + lane * 4;
+  return Angles{*(const f4v*)(p.cos + at), *(const f4v*)(p.sin + at)};
 }
-// v c + pair(v) s; `other`: the lane that holds the pairs
+// (a, b) turned by the angles (sign -1: back)
 template <bool PAIRS>
-__device__ __forceinline__ f8v rotate(f8v v, const Angles& a, float sign, int other) {
-  f8v w;
+__device__ __forceinline__ void rotate(f4v& a, f4v& b, const Angles& x, float sign) {
+  const f4v s = x.s * sign;
   if constexpr (PAIRS) {
-    w = __builtin_shufflevector(v, v, 1, 0, 3, 2, 5, 4, 7, 6);
-  } else {
+    const f4v u = a, v = b;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) w[i] = __shfl(v[i], other);
+    for (int i = 0; i < 2; ++i) {
+      a[2 * i] = u[2 * i] * x.c[i] - u[2 * i + 1] * s[i];
+      a[2 * i + 1] = u[2 * i + 1] * x.c[i] + u[2 * i] * s[i];
+      b[2 * i] = v[2 * i] * x.c[2 + i] - v[2 * i + 1] * s[2 + i];
+      b[2 * i + 1] = v[2 * i + 1] * x.c[2 + i] + v[2 * i] * s[2 + i];
+    }
+  } else {
+    const f4v u = a;
+    a = u * x.c - b * s;
+    b = b * x.c + u * s;
   }
-  return v * a.c + w * (a.s * sign);
 }
 
 // Which rows a lane group runs: HP heads of one token at a time.
@@ -128,28 +126,37 @@ __global__ __launch_bounds__(256) void k_norm_fwd(const NormProblem p, const Nor
   const unsigned blk = isq ? blockIdx.x : blockIdx.x - qblocks;
   const int lane = threadIdx.x % L;
   const Rows<L, HP> r(p, x.heads, blk * (256 / L) + threadIdx.x / L);
-  const bool in = lane * 8 < p.D;
-  const TIn* xp = (const TIn*)x.x.p + r.b * x.x.sb + r.t * x.x.st + r.h0 * x.x.sh + lane * 8;
-  f8v v[HP];
+  const Place at = place_of<PAIRS>(p, lane);
+  const f4v zero = {0.f, 0.f, 0.f, 0.f}, one = {1.f, 1.f, 1.f, 1.f};
+  const TIn* xp = (const TIn*)x.x.p + r.b * x.x.sb + r.t * x.x.st + r.h0 * x.x.sh;
+  f4v u[HP], v[HP];
 #pragma unroll
   for (int j = 0; j < HP; ++j) {
-    v[j] = f8v{0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (in && j < r.nh) v[j] = load8<TIn>(xp + j * x.x.sh);
+    u[j] = zero;
+    v[j] = zero;
+    if (at.in && j < r.nh) {
+      u[j] = load4<TIn>(xp + j * x.x.sh + at.a);
+      v[j] = load4<TIn>(xp + j * x.x.sh + at.b);
+    }
   }
-  f8v w = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  Angles a{w, w};
-  if (in && r.nh) {
-    a = load_angles<PAIRS>(p, r.b, r.t, lane);
-    w = load_weight(x.w, p.wtype, lane * 8);
+  Angles ang{one, zero};
+  f4v wu = zero, wv = zero;
+  if (at.in && r.nh) {
+    if (at.rotated) ang = load_angles(p, r.b, r.t, lane);
+    wu = load_weight(x.w, p.wtype, at.a);
+    wv = load_weight(x.w, p.wtype, at.b);
   }
-  const int half = p.rot / 16, other = (threadIdx.x & 63) + (lane < half ? half : lane < 2 * half ? -half : 0);
-  TIn* yp = (TIn*)x.y + ((r.b * p.T + r.t) * x.heads + r.h0) * p.D + lane * 8;
+  TIn* yp = (TIn*)x.y + ((r.b * p.T + r.t) * x.heads + r.h0) * p.D;
   const float inv = 1.f / (float)p.D;
 #pragma unroll
   for (int j = 0; j < HP; ++j) {
-    const float rs = 1.f / sqrtf(row_sum<L>(dot8(v[j], v[j])) * inv + p.eps);
-    const f8v y = rotate<PAIRS>(v[j] * rs * w, a, 1.f, other);
-    if (in && j < r.nh) store8<TIn>(yp + (int64_t)j * p.D, y);
+    const float rs = rsqrtf(row_sum<L>(dot4(u[j], u[j]) + dot4(v[j], v[j])) * inv + p.eps);
+    f4v a = u[j] * rs * wu, b = v[j] * rs * wv;
+    rotate<PAIRS>(a, b, ang, 1.f);
+    if (at.in && j < r.nh) {
+      store4<TIn>(yp + (int64_t)j * p.D + at.a, a);
+      store4<TIn>(yp + (int64_t)j * p.D + at.b, b);
+    }
   }
 }
 
@@ -165,45 +172,60 @@ __global__ __launch_bounds__(256) void k_norm_bwd(const NormProblem p, const Nor
   const NormSide& x = isq ? q : k;
   const unsigned blk = isq ? blockIdx.x : blockIdx.x - qblocks, nblk = isq ? qblocks : gridDim.x - qblocks;
   const int lane = threadIdx.x % L;
-  const bool in = lane * 8 < p.D;
-  const f8v zero = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-  const f8v w = in ? load_weight(x.w, p.wtype, lane * 8) : zero;
-  const int half = p.rot / 16, other = (threadIdx.x & 63) + (lane < half ? half : lane < 2 * half ? -half : 0);
+  const Place at = place_of<PAIRS>(p, lane);
+  const f4v zero = {0.f, 0.f, 0.f, 0.f}, one = {1.f, 1.f, 1.f, 1.f};
+  const f4v wu = at.in ? load_weight(x.w, p.wtype, at.a) : zero, wv = at.in ? load_weight(x.w, p.wtype, at.b) : zero;
   const float inv = 1.f / (float)p.D;
   const int64_t groups = p.B * p.T * ((x.heads + HP - 1) / HP);
-  f8v dw = zero;
+  f4v du = zero, dv = zero;
   for (int64_t g0 = (int64_t)blk * G; g0 < groups; g0 += (int64_t)nblk * G) {
     const Rows<L, HP> r(p, x.heads, (uint32_t)g0 + threadIdx.x / L);
-    const TIn* xp = (const TIn*)x.x.p + r.b * x.x.sb + r.t * x.x.st + r.h0 * x.x.sh + lane * 8;
-    const TIn* dp = (const TIn*)x.dy.p + r.b * x.dy.sb + r.t * x.dy.st + r.h0 * x.dy.sh + lane * 8;
-    f8v v[HP], d[HP];
+    const TIn* xp = (const TIn*)x.x.p + r.b * x.x.sb + r.t * x.x.st + r.h0 * x.x.sh;
+    const TIn* dp = (const TIn*)x.dy.p + r.b * x.dy.sb + r.t * x.dy.st + r.h0 * x.dy.sh;
+    f4v u[HP], v[HP], a[HP], b[HP];
 #pragma unroll
     for (int j = 0; j < HP; ++j) {
+      u[j] = zero;
       v[j] = zero;
-      d[j] = zero;
-      if (in && j < r.nh) {
-        v[j] = load8<TIn>(xp + j * x.x.sh);
-        d[j] = load8<TIn>(dp + j * x.dy.sh);
+      a[j] = zero;
+      b[j] = zero;
+      if (at.in && j < r.nh) {
+        u[j] = load4<TIn>(xp + j * x.x.sh + at.a);
+        v[j] = load4<TIn>(xp + j * x.x.sh + at.b);
+        a[j] = load4<TIn>(dp + j * x.dy.sh + at.a);
+        b[j] = load4<TIn>(dp + j * x.dy.sh + at.b);
       }
     }
-    Angles a{zero, zero};
-    if (in && r.nh) a = load_angles<PAIRS>(p, r.b, r.t, lane);
-    TIn* yp = (TIn*)x.y + ((r.b * p.T + r.t) * x.heads + r.h0) * p.D + lane * 8;
+    Angles ang{one, zero};
+    if (at.rotated && r.nh) ang = load_angles(p, r.b, r.t, lane);
+    TIn* yp = (TIn*)x.y + ((r.b * p.T + r.t) * x.heads + r.h0) * p.D;
 #pragma unroll
     for (int j = 0; j < HP; ++j) {
-      const f8v dn = rotate<PAIRS>(d[j], a, -1.f, other);
-      const float rs = 1.f / sqrtf(row_sum<L>(dot8(v[j], v[j])) * inv + p.eps);
-      const f8v hat = v[j] * rs, t = dn * w;
-      const float m = row_sum<L>(dot8(t, hat)) * inv;
-      if (j < r.nh) dw += dn * hat;
-      if (in && j < r.nh) store8<TIn>(yp + (int64_t)j * p.D, (t - hat * m) * rs);
+      rotate<PAIRS>(a[j], b[j], ang, -1.f);
+      const float rs = rsqrtf(row_sum<L>(dot4(u[j], u[j]) + dot4(v[j], v[j])) * inv + p.eps);
+      const f4v hu = u[j] * rs, hv = v[j] * rs, tu = a[j] * wu, tv = b[j] * wv;
+      const float m = row_sum<L>(dot4(tu, hu) + dot4(tv, hv)) * inv;
+      if (j < r.nh) {
+        du += a[j] * hu;
+        dv += b[j] * hv;
+        if (at.in) {
+          store4<TIn>(yp + (int64_t)j * p.D + at.a, (tu - hu * m) * rs);
+          store4<TIn>(yp + (int64_t)j * p.D + at.b, (tv - hv * m) * rs);
+        }
+      }
     }
   }
+  if (at.in) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) sums[threadIdx.x / L][lane * 8 + i] = dw[i];
+    for (int i = 0; i < 4; ++i) {
+      sums[threadIdx.x / L][at.a + i] = du[i];
+      sums[threadIdx.x / L][at.b + i] = dv[i];
+    }
+  }
   __syncthreads();
   if ((int)threadIdx.x < p.D) {
     float s = 0.f;
+#pragma unroll
     for (int g = 0; g < G; ++g) s += sums[g][threadIdx.x];
     partial[(int64_t)blockIdx.x * p.D + threadIdx.x] = s;
   }
@@ -220,6 +242,7 @@ __global__ __launch_bounds__(256) void k_norm_weights(const float* partial, int 
   const int c = threadIdx.x & 7, r = threadIdx.x >> 3, col = (int)(blockIdx.x % parts) * 8 + c;
   const unsigned first = isq ? 0 : qblocks, n = isq ? qblocks : kblocks;
   float s = 0.f;
+#pragma unroll 8
   for (unsigned i = r; i < n; i += 32) s += partial[(int64_t)(first + i) * D + col];
   sums[r][c] = s;
   __syncthreads();
