@@ -14,6 +14,7 @@ Entry points (same names as the C ABI):
     scan_log_fwd_gated / scan_log_bwd_gated (log a = -softplus(z)) -> h / (dz, dlog_b, dlog_h0)
     matrix_affine_scan_fwd(A, B, h0=None, cu_seqlens=None, reverse=False) -> h
     matrix_affine_scan_bwd(A, h, dy, h0=None, cu_seqlens=None, reverse=False) -> (dA, dB, dh0)
+    linear_attention_fwd / _bwd / _step, qk_norm_rope_fwd / _bwd (layouts: see _attention.py)
 
 Scalar tensors are [..., T] (every leading axis is an independent row, time
 contiguous); matrix tensors are [..., T, k, k] and [..., T, k, v]. ``h0`` is
@@ -36,6 +37,7 @@ __all__ = [
     "scan_fwd_gated", "scan_bwd_gated", "scan_log_fwd_gated", "scan_log_bwd_gated",
     "scan_causal", "scan_bidirectional_branched", "scan_log", "matrix_scan", "GATE_SIGMOID", "GATE_NEG_SOFTPLUS",
     "workspace_bytes", "OP_SCAN_FWD", "OP_SCAN_BWD", "OP_SCAN_LOG_FWD", "OP_MATRIX_FWD", "OP_MATRIX_BWD",
+    "linear_attention", "qk_norm_rope", "rotary_linear_attention", "rotary_linear_attention_step",
     "linear_attention_fwd", "linear_attention_bwd", "linear_attention_step", "qk_norm_rope_fwd", "qk_norm_rope_bwd",
     "OP_SCAN_LOG_BWD", "set_debug", "debug_enabled", "workspace_error", "stream_ceiling", "release_capture_workspaces",
 ]
@@ -636,6 +638,41 @@ def scan_log(log_a, log_b, log_h0=None, cu_seqlens=None, reverse=False):
 def matrix_scan(A, B, h0=None, cu_seqlens=None, reverse=False):
     """Differentiable matrix-affine scan h_t = A_t h_{t-1} + B_t."""
     return torch.ops.mscan.matrix_scan(A, B, h0, cu_seqlens, reverse)
+
+
+def linear_attention(q, k, v, g, h0=None, cu_seqlens=None, scale=None):
+    """Differentiable linear attention with a decay for each head: (o, ht) of
+    S_t = e^{g_t} S_{t-1} + k_t v_t^T, o_t = scale S_t^T q_t (linear_attention_fwd),
+    with native kernels for the gradients of q, k, v, g and h0."""
+    return torch.ops.mscan.linear_attention(q, k, v, g, h0, cu_seqlens, q.shape[-1] ** -0.5 if scale is None else scale)
+
+
+def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6, interleaved=False):
+    """Differentiable RMS norm of queries and keys for each head with the position
+    rotation (qk_norm_rope_fwd), with native kernels for the gradients of q, k and
+    the weights."""
+    return torch.ops.mscan.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+
+
+def rotary_linear_attention(q, k, v, g, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, h0=None,
+                            cu_seqlens=None, scale=None, eps=1e-6, interleaved=False):
+    """The mixer of a linear attention layer on a projection's heads: queries and
+    keys normed and rotated (qk_norm_rope), then linear attention. (o, ht),
+    differentiable. Packed sequences count their positions from their starts
+    only if `positions` says so."""
+    q, k = qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
+    return linear_attention(q, k, v, g, h0, cu_seqlens, scale)
+
+
+def rotary_linear_attention_step(q, k, v, g, state, q_weight=None, k_weight=None, cos=None, sin=None, positions=None,
+                                 slots=None, scale=None, eps=1e-6, interleaved=False):
+    """One token of rotary_linear_attention for each sequence, q, k [B, Hk, Dk],
+    against a pool of states updated in place (linear_attention_step).
+    positions: [B], the tokens' positions."""
+    q, k = torch.ops.mscan.qk_norm_rope(q[:, None], k[:, None], q_weight, k_weight, cos, sin,
+                                        None if positions is None else positions[:, None], eps, interleaved)
+    return torch.ops.mscan.linear_attention_step(q[:, 0], k[:, 0], v, g, state, slots,
+                                                 q.shape[-1] ** -0.5 if scale is None else scale)
 
 
 def matrix_cumprod(A, cu_seqlens=None, reverse=False):

@@ -11,6 +11,12 @@ Ops (namespace ``mscan``):
     scan_log_backward(log_a, log_b, h, dy, log_h0?, cu_seqlens?, reverse, need_dh0) -> (dlog_a, dlog_b, dlog_h0)
     matrix_scan(A, B, h0?, cu_seqlens?, reverse) -> h
     matrix_scan_backward(A, h, dy, h0?, cu_seqlens?, reverse, need_dh0) -> (dA, dB, dh0)
+    linear_attention(q, k, v, g, h0?, cu_seqlens?, scale) -> (o, ht)
+    linear_attention_backward(q, k, v, g, do, h0?, dht?, cu_seqlens?, scale, need_dg, need_dh0) -> (dq, dk, dv, dg, dh0)
+    linear_attention_step(q, k, v, g, state, slots?, scale) -> o                       (state is updated in place)
+    qk_norm_rope(q, k, q_weight?, k_weight?, cos?, sin?, positions?, eps, interleaved) -> (q', k')
+    qk_norm_rope_backward(q, k, q_weight?, k_weight?, cos?, sin?, dq', dk', positions?, eps, interleaved, need_dw)
+        -> (dq, dk, dq_weight, dk_weight)
 A custom op cannot return None, so a skipped dh0 comes back as an empty tensor.
 Every op runs the library's HIP kernels; there is no other implementation.
 """
@@ -21,7 +27,8 @@ from typing import Optional, Tuple
 import torch
 from torch import Tensor
 
-from . import (matrix_affine_scan_bwd, matrix_affine_scan_fwd, scan_bwd, scan_fwd, scan_log_bwd,
+from . import (linear_attention_bwd, linear_attention_fwd, linear_attention_step, matrix_affine_scan_bwd,
+               matrix_affine_scan_fwd, qk_norm_rope_bwd, qk_norm_rope_fwd, scan_bwd, scan_fwd, scan_log_bwd,
                scan_log_fwd)
 
 
@@ -174,3 +181,134 @@ def _matrix_backward(ctx, dy):
 
 
 matrix_scan_op.register_autograd(_matrix_backward, setup_context=_matrix_setup)
+
+
+# ---------------------------------------------------------------------------
+# linear attention
+# ---------------------------------------------------------------------------
+def _nothing(like: Tensor) -> Tensor:
+    return like.new_empty((0,), dtype=torch.float32)
+
+
+def _states_like(q: Tensor, v: Tensor, cu: Optional[Tensor]) -> Tensor:
+    n = q.shape[0] if cu is None else cu.shape[0] - 1
+    return torch.empty((n, v.shape[2], q.shape[3], v.shape[3]), dtype=torch.float32, device=q.device)
+
+
+def _grad_rows(t: Optional[Tensor], like: Tensor) -> Tensor:
+    """An incoming gradient in the layout that the kernels read."""
+    if t is None:
+        return torch.zeros(like.shape, dtype=like.dtype, device=like.device)
+    return t.contiguous()
+
+
+@torch.library.custom_op("mscan::linear_attention", mutates_args=())
+def linear_attention_op(q: Tensor, k: Tensor, v: Tensor, g: Tensor, h0: Optional[Tensor],
+                        cu_seqlens: Optional[Tensor], scale: float) -> Tuple[Tensor, Tensor]:
+    return linear_attention_fwd(q, k, v, g, h0=h0, cu_seqlens=cu_seqlens, scale=scale)
+
+
+@linear_attention_op.register_fake
+def _(q, k, v, g, h0, cu_seqlens, scale):
+    return torch.empty(v.shape, dtype=v.dtype, device=v.device), _states_like(q, v, cu_seqlens)
+
+
+@torch.library.custom_op("mscan::linear_attention_backward", mutates_args=())
+def linear_attention_backward_op(q: Tensor, k: Tensor, v: Tensor, g: Tensor, do: Tensor, h0: Optional[Tensor],
+                                 dht: Optional[Tensor], cu_seqlens: Optional[Tensor], scale: float, need_dg: bool,
+                                 need_dh0: bool) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
+    dq, dk, dv, dg, dh0 = linear_attention_bwd(q, k, v, g, do, h0=h0, dht=dht, cu_seqlens=cu_seqlens, scale=scale,
+                                               need_dg=need_dg, need_dh0=need_dh0)
+    return dq, dk, dv, dg if need_dg else _nothing(g), dh0 if need_dh0 else _nothing(g)
+
+
+@linear_attention_backward_op.register_fake
+def _(q, k, v, g, do, h0, dht, cu_seqlens, scale, need_dg, need_dh0):
+    dq, dk, dv = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k, v))
+    dg = torch.empty(g.shape, dtype=torch.float32, device=g.device) if need_dg else _nothing(g)
+    return dq, dk, dv, dg, _states_like(q, v, cu_seqlens) if need_dh0 else _nothing(g)
+
+
+def _attention_setup(ctx, inputs, output):
+    q, k, v, g, h0, cu, scale = inputs
+    ctx.save_for_backward(q, k, v, g, h0, cu)
+    ctx.scale = scale
+    ctx.set_materialize_grads(False)
+
+
+def _attention_backward(ctx, do, dht):
+    q, k, v, g, h0, cu = ctx.saved_tensors
+    if do is None and dht is None:
+        return (None,) * 7
+    need_g, need_h = ctx.needs_input_grad[3], h0 is not None and ctx.needs_input_grad[4]
+    dq, dk, dv, dg, dh0 = linear_attention_backward_op(
+        q, k, v, g, _grad_rows(do, v), h0, None if dht is None else dht.contiguous(), cu, ctx.scale, need_g, need_h)
+    return dq, dk, dv, dg if need_g else None, dh0 if need_h else None, None, None
+
+
+linear_attention_op.register_autograd(_attention_backward, setup_context=_attention_setup)
+
+
+@torch.library.custom_op("mscan::linear_attention_step", mutates_args=("state",))
+def linear_attention_step_op(q: Tensor, k: Tensor, v: Tensor, g: Tensor, state: Tensor, slots: Optional[Tensor],
+                             scale: float) -> Tensor:
+    return linear_attention_step(q, k, v, g, state, slots=slots, scale=scale)
+
+
+@linear_attention_step_op.register_fake
+def _(q, k, v, g, state, slots, scale):
+    return torch.empty(v.shape, dtype=v.dtype, device=v.device)
+
+
+# ---------------------------------------------------------------------------
+# query / key norm with rotation
+# ---------------------------------------------------------------------------
+@torch.library.custom_op("mscan::qk_norm_rope", mutates_args=())
+def qk_norm_rope_op(q: Tensor, k: Tensor, q_weight: Optional[Tensor], k_weight: Optional[Tensor],
+                    cos: Optional[Tensor], sin: Optional[Tensor], positions: Optional[Tensor], eps: float,
+                    interleaved: bool) -> Tuple[Tensor, Tensor]:
+    return qk_norm_rope_fwd(q, k, q_weight, k_weight, cos, sin, positions=positions, eps=eps, interleaved=interleaved)
+
+
+@qk_norm_rope_op.register_fake
+def _(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved):
+    return tuple(torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+
+
+@torch.library.custom_op("mscan::qk_norm_rope_backward", mutates_args=())
+def qk_norm_rope_backward_op(q: Tensor, k: Tensor, q_weight: Optional[Tensor], k_weight: Optional[Tensor],
+                             cos: Optional[Tensor], sin: Optional[Tensor], dyq: Tensor, dyk: Tensor,
+                             positions: Optional[Tensor], eps: float, interleaved: bool,
+                             need_dw: bool) -> Tuple[Tensor, Tensor, Tensor, Tensor]:
+    dq, dk, dwq, dwk = qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, dyq, dyk, positions=positions, eps=eps,
+                                        interleaved=interleaved, need_dw=need_dw)
+    return dq, dk, _nothing(q) if dwq is None else dwq, _nothing(k) if dwk is None else dwk
+
+
+@qk_norm_rope_backward_op.register_fake
+def _(q, k, q_weight, k_weight, cos, sin, dyq, dyk, positions, eps, interleaved, need_dw):
+    dq, dk = (torch.empty(x.shape, dtype=x.dtype, device=x.device) for x in (q, k))
+    if q_weight is None or not need_dw:
+        return dq, dk, _nothing(q), _nothing(k)
+    return dq, dk, q.new_empty(q.shape[3:], dtype=torch.float32), q.new_empty(q.shape[3:], dtype=torch.float32)
+
+
+def _norm_setup(ctx, inputs, output):
+    q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved = inputs
+    ctx.save_for_backward(q, k, q_weight, k_weight, cos, sin, positions)
+    ctx.eps, ctx.interleaved = eps, interleaved
+    ctx.set_materialize_grads(False)
+
+
+def _norm_backward(ctx, dyq, dyk):
+    q, k, q_weight, k_weight, cos, sin, positions = ctx.saved_tensors
+    if dyq is None and dyk is None:
+        return (None,) * 9
+    need = q_weight is not None and (ctx.needs_input_grad[2] or ctx.needs_input_grad[3])
+    dq, dk, dwq, dwk = qk_norm_rope_backward_op(q, k, q_weight, k_weight, cos, sin, _grad_rows(dyq, q), _grad_rows(dyk, k),
+                                                positions, ctx.eps, ctx.interleaved, need)
+    return (dq, dk, dwq.to(q_weight.dtype) if need else None, dwk.to(k_weight.dtype) if need else None, None, None, None,
+            None, None)
+
+
+qk_norm_rope_op.register_autograd(_norm_backward, setup_context=_norm_setup)

@@ -33,7 +33,7 @@ mscan_status check(const mscan_attention* p) {
   return MSCAN_OK;
 }
 
-LaProblem problem(const mscan_attention* p, const float* g, bool backward) {
+LaProblem problem(const mscan_attention* p, const float* g) {
   LaProblem r{};
   r.B = p->B;
   r.T = p->T;
@@ -48,7 +48,7 @@ LaProblem problem(const mscan_attention* p, const float* g, bool backward) {
   r.gsb = p->g_strides[0];
   r.gst = p->g_strides[1];
   r.gsh = p->g_strides[2];
-  mscan::la::plan(r, backward);
+  mscan::la::plan(r);
   return r;
 }
 
@@ -149,7 +149,7 @@ extern "C" {
 
 size_t linear_attention_workspace_bytes(const mscan_attention* prob, int backward) {
   if (check(prob) != MSCAN_OK || backward < 0 || backward > 1) return 0;
-  const LaProblem r = problem(prob, nullptr, backward == 1);
+  const LaProblem r = problem(prob, nullptr);
   if (check_blocks(r) != MSCAN_OK) return 0;
   return (backward ? bwd_space(r).bytes : fwd_space(r).bytes) + 256;
 }
@@ -161,7 +161,7 @@ mscan_status linear_attention_fwd(const mscan_attention* prob, int dtype, const 
   if (s != MSCAN_OK) return s;
   if (dtype != MSCAN_F32 && dtype != MSCAN_BF16 && dtype != MSCAN_F16) return MSCAN_ERR_UNSUPPORTED;
   mscan::la::FwdArgs a{};
-  a.pr = problem(prob, g, false);
+  a.pr = problem(prob, g);
   const int share = prob->H / prob->Hk;
   if ((s = heads(q, dtype, share, prob->Dk, a.q)) != MSCAN_OK) return s;
   if ((s = heads(k, dtype, share, prob->Dk, a.k)) != MSCAN_OK) return s;
@@ -187,7 +187,7 @@ mscan_status linear_attention_bwd(const mscan_attention* prob, int dtype, const 
   if (s != MSCAN_OK) return s;
   if (dtype != MSCAN_F32 && dtype != MSCAN_BF16 && dtype != MSCAN_F16) return MSCAN_ERR_UNSUPPORTED;
   mscan::la::BwdArgs a{};
-  a.pr = problem(prob, g, true);
+  a.pr = problem(prob, g);
   const int share = prob->H / prob->Hk;
   if ((s = heads(q, dtype, share, prob->Dk, a.q)) != MSCAN_OK) return s;
   if ((s = heads(k, dtype, share, prob->Dk, a.k)) != MSCAN_OK) return s;

@@ -154,7 +154,7 @@ hipError_t launch_join(const LaProblem& p, bool rev, const float* outer, float* 
 // one after the other in as many rounds as the card's 512 places ask for, 0.45 of
 // that for the pass that gives the spans' own states, a round's start, and about
 // two chunks for the join and the launches.
-void plan(LaProblem& p, bool backward) {
+void plan(LaProblem& p) {
   const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H;
   const auto cost = [&](int64_t span) {
     const int64_t n = (p.T + span - 1) / span, blocks = n * rows;
