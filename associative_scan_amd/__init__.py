@@ -97,7 +97,7 @@ def load_library(path: str):
         "mscan_stream_ceiling": (i32, [ctypes.POINTER(p), i32, ctypes.POINTER(p), i32, sz, p]),
         "mscan_debug_partial_fwd": (i32, [P, i32, i32, p, p, p, p, sz, ctypes.c_int64, ctypes.c_int64, ctypes.c_uint32,
                                           p]),
-        "linear_attention_workspace_bytes": (sz, [p, i32]),
+        "linear_attention_workspace_bytes": (sz, [p, i32, i32]),
         "linear_attention_fwd": (i32, [p, i32, p, p, p, p, p, p, p, p, sz, p]),
         "linear_attention_bwd": (i32, [p, i32, p, p, p, p, p, p, p, p, p, p, p, i32, p, p, sz, p]),
         "linear_attention_step": (i32, [p, i32, p, p, p, p, p, ctypes.c_int32, p, p, p]),

@@ -120,10 +120,10 @@ def _states(t, shape, name, dev):
     return t
 
 
-def _space(prob, backward, dev):
+def _space(prob, dtype, backward, dev):
     """A workspace of the call's own: torch's allocator keeps it in the stream's
     order, and in a captured graph's own pool."""
-    need = lib.linear_attention_workspace_bytes(prob, backward)
+    need = lib.linear_attention_workspace_bytes(prob, dtype, backward)
     if need <= 256:
         return None, 0
     return torch.empty(need, dtype=torch.uint8, device=dev), need
@@ -143,7 +143,7 @@ def linear_attention_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=None, need_
             ht.zero_() if h0 is None else ht.copy_(h0)
         return o, ht
     with _on(dev):
-        ws, n = _space(prob, 0, dev)
+        ws, n = _space(prob, dt, 0, dev)
         _check("linear_attention_fwd", lib.linear_attention_fwd(
             prob, dt, qh, kh, vh, g.data_ptr(), _ptr(h0), o.data_ptr(), _ptr(ht), _ptr(ws), n, _stream_handle(dev)))
     return o, ht
@@ -169,7 +169,7 @@ def linear_attention_bwd(q, k, v, g, do, h0=None, dht=None, cu_seqlens=None, sca
             dh0.zero_() if dht is None else dh0.copy_(dht)
         return dq, dk, dv, dg, dh0
     with _on(dev):
-        ws, n = _space(prob, 1, dev)
+        ws, n = _space(prob, dt, 1, dev)
         _check("linear_attention_bwd", lib.linear_attention_bwd(
             prob, dt, qh, kh, vh, g.data_ptr(), oh, _ptr(h0), _ptr(dht), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
             int(g.dim() == 1), _ptr(dh0), _ptr(ws), n, _stream_handle(dev)))

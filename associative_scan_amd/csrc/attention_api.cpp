@@ -33,7 +33,7 @@ mscan_status check(const mscan_attention* p) {
   return MSCAN_OK;
 }
 
-LaProblem problem(const mscan_attention* p, const float* g) {
+LaProblem problem(const mscan_attention* p, const float* g, int dtype, bool backward) {
   LaProblem r{};
   r.B = p->B;
   r.T = p->T;
@@ -48,7 +48,7 @@ LaProblem problem(const mscan_attention* p, const float* g) {
   r.gsb = p->g_strides[0];
   r.gst = p->g_strides[1];
   r.gsh = p->g_strides[2];
-  mscan::la::plan(r);
+  mscan::la::plan(r, dtype, backward);
   return r;
 }
 
@@ -147,9 +147,10 @@ bool weight_aligned(const void* w, int dtype) { return ((uintptr_t)w & (dtype ==
 
 extern "C" {
 
-size_t linear_attention_workspace_bytes(const mscan_attention* prob, int backward) {
+size_t linear_attention_workspace_bytes(const mscan_attention* prob, int dtype, int backward) {
   if (check(prob) != MSCAN_OK || backward < 0 || backward > 1) return 0;
-  const LaProblem r = problem(prob, nullptr);
+  if (dtype != MSCAN_F32 && dtype != MSCAN_BF16 && dtype != MSCAN_F16) return 0;
+  const LaProblem r = problem(prob, nullptr, dtype, backward == 1);
   if (check_blocks(r) != MSCAN_OK) return 0;
   return (backward ? bwd_space(r).bytes : fwd_space(r).bytes) + 256;
 }
@@ -161,7 +162,7 @@ mscan_status linear_attention_fwd(const mscan_attention* prob, int dtype, const 
   if (s != MSCAN_OK) return s;
   if (dtype != MSCAN_F32 && dtype != MSCAN_BF16 && dtype != MSCAN_F16) return MSCAN_ERR_UNSUPPORTED;
   mscan::la::FwdArgs a{};
-  a.pr = problem(prob, g);
+  a.pr = problem(prob, g, dtype, false);
   const int share = prob->H / prob->Hk;
   if ((s = heads(q, dtype, share, prob->Dk, a.q)) != MSCAN_OK) return s;
   if ((s = heads(k, dtype, share, prob->Dk, a.k)) != MSCAN_OK) return s;
@@ -187,7 +188,7 @@ mscan_status linear_attention_bwd(const mscan_attention* prob, int dtype, const 
   if (s != MSCAN_OK) return s;
   if (dtype != MSCAN_F32 && dtype != MSCAN_BF16 && dtype != MSCAN_F16) return MSCAN_ERR_UNSUPPORTED;
   mscan::la::BwdArgs a{};
-  a.pr = problem(prob, g);
+  a.pr = problem(prob, g, dtype, true);
   const int share = prob->H / prob->Hk;
   if ((s = heads(q, dtype, share, prob->Dk, a.q)) != MSCAN_OK) return s;
   if ((s = heads(k, dtype, share, prob->Dk, a.k)) != MSCAN_OK) return s;

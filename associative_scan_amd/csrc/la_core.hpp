@@ -7,48 +7,68 @@
 namespace mscan {
 namespace la {
 
-// Chunk sizes: 64 steps for 16-bit math; 32 for fp32 math, whose tiles are
-// twice as wide and whose products within a chunk cost sixteen times as much.
-template <class TM>
-constexpr int kChunk = sizeof(TM) == 2 ? 64 : 32;
-// Pieces of the masked scores: bf16 alone would be as coarse as a bf16 output.
-template <class TM>
-constexpr int kPiecesP = sizeof(TM) == 2 ? 2 : 1;
-// Pieces of the injected values and of the state as an operand. Three keep
-// fp32 states and gate gradients to fp32; two are enough for 16-bit outputs.
-template <class TM>
-constexpr int kPiecesZ = sizeof(TM) == 2 ? 3 : 1;
-template <class TM>
-constexpr int kPiecesX = sizeof(TM) == 2 ? 2 : 1;
-template <class TM>
-constexpr int kPiecesXExact = sizeof(TM) == 2 ? 3 : 1;
+// Steps of a chunk: inputs in several planes take 32, for their tiles' sake.
+template <class T>
+constexpr int kChunk = kPlanes<T> == 1 ? 64 : 32;
+// Pieces of the masked scores. One would be as coarse as a bf16 output.
+template <class T>
+constexpr int kPiecesP = kPlanes<T> == 3 ? 3 : 2;
+// Pieces of the state as an operand: two are enough for a 16-bit output, three
+// keep the gates' gradients (EXACT) and fp32 outputs to fp32. The injected values
+// always have three, which keeps states to fp32.
+template <class T, bool EXACT>
+constexpr int kPiecesS = EXACT || kPlanes<T> == 3 ? 3 : 2;
+constexpr int kPiecesZ = 3;
 
 // A lane's offsets into the tiles (see la_device.hpp).
-template <class TM, int C, int DX, int DZ>
+template <int C, int DX, int DZ>
 struct LaneOffsets {
   int x32, x16, y, z, p;
   __device__ __forceinline__ explicit LaneOffsets(int z0)
-      : x32(row_lane<TM, DX, 32>()), x16(row_lane<TM, DX, 16>()), y(col_lane<TM, DX, true>()),
-        z(moved<TM, DZ>(col_lane<TM, DZ, false>(), 0, z0 / kUnit<TM>)), p(row_lane<TM, C, 32>()) {}
+      : x32(row_lane<DX, 32>()), x16(row_lane<DX, 16>()), y(col_lane<DX, true>()),
+        z(moved<bf16, DZ>(col_lane<DZ, false>(), 0, z0 / 8)), p(row_lane<C, 32>()) {}
 };
 
 // One 16 x 16 tile of the scores x_r . y_c, transposed: rows ct*16 + 4 (l / 16)
-// + i, i < 4, are steps c, column rt*16 + (l & 15) is step r.
-template <class TM, int DX>
+// + i, i < 4, are steps c, column rt*16 + (l & 15) is step r. One plane's
+// fragments can be read ahead; several are read as the product goes.
+template <int PL, int C, int DX>
 struct ScoreFrags {
-  typename Math<TM>::Frag x[DX / 32], y[DX / 32];
-  __device__ __forceinline__ void read(const TM* X, const TM* Y, int x16, int rt, int ct) {
-    // 16 rows leave the units' order as it is
+  static constexpr int N = DX / 32;
+  bf8 x[PL][PL == 1 ? N : 2], y[PL][PL == 1 ? N : 2];
+  const bf16 *px, *py;
+  int off;
+  __device__ __forceinline__ void read_step(int i, int slot) {
 #pragma unroll
-    for (int i = 0; i < DX / 32; ++i) {
-      y[i] = row_frag<TM, DX>(Y + ct * 16 * DX, x16, 0, i * 32);
-      x[i] = row_frag<TM, DX>(X + rt * 16 * DX, x16, 0, i * 32);
+    for (int p = 0; p < PL; ++p) {
+      y[p][slot] = row_frag<DX>(py + p * C * DX, off, 0, i * 32);
+      x[p][slot] = row_frag<DX>(px + p * C * DX, off, 0, i * 32);
     }
   }
-  __device__ __forceinline__ f4v product() const {
+  __device__ __forceinline__ void read(const bf16* X, const bf16* Y, int x16, int rt, int ct) {
+    // 16 rows leave the units' order as it is
+    px = X + rt * 16 * DX;
+    py = Y + ct * 16 * DX;
+    off = x16;
+#pragma unroll
+    for (int i = 0; i < (PL == 1 ? N : 1); ++i) read_step(i, i);
+  }
+  __device__ __forceinline__ f4v product() {
     f4v acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int i = 0; i < DX / 32; ++i) acc = Math<TM>::mma16(y[i], x[i], acc);
+    for (int i = 0; i < N; ++i) {
+      if constexpr (PL > 1) {
+        step_fence();
+        if (i + 1 < N) read_step(i + 1, (i + 1) & 1);
+        step_fence();
+      }
+      const int slot = PL == 1 ? i : i & 1;
+#pragma unroll
+      for (int p = 0; p < PL; ++p)
+#pragma unroll
+        for (int q = 0; q < PL; ++q)
+          if (p + q < 3) acc = mma16(y[p][slot], x[q][slot], acc);
+    }
     return acc;
   }
 };
@@ -69,13 +89,13 @@ __device__ __forceinline__ f4v decay_tile(const Decays<C>& d, int rt, int ct, in
   return o;
 }
 // Masked scores into P [NP][C][C] (row r, column c).
-template <class TM, int C, int NP>
-__device__ __forceinline__ void put_tile(TM* P, f4v val, int rt, int ct, int l) {
-  const int off = cell_at<TM, C>(rt * 16 + (l & 15), ct * 16 + ((l >> 4) << 2));
-  typename Four<TM>::type piece[NP];
-  split4<TM, NP>(val, piece);
+template <int C, int NP>
+__device__ __forceinline__ void put_tile(bf16* P, f4v val, int rt, int ct, int l) {
+  const int off = cell_at<bf16, C>(rt * 16 + (l & 15), ct * 16 + ((l >> 4) << 2));
+  u2v piece[NP];
+  split4<NP>(val, piece);
 #pragma unroll
-  for (int p = 0; p < NP; ++p) *(typename Four<TM>::type*)(P + p * C * C + off) = piece[p];
+  for (int p = 0; p < NP; ++p) *(u2v*)(P + p * C * C + off) = piece[p];
 }
 // The 16 x 16 tiles that a product over P reads: for every 32 rows, the columns
 // up to their end (REV: from their start). Tile i of kTiles<C>.
@@ -97,13 +117,14 @@ __device__ __forceinline__ void tile_of(int i, int& rt, int& ct) {
     }
   }
 }
-template <class TM, int C, int DX, int NP, bool REV, int WAVES>
-__device__ __forceinline__ void scores(const TM* X, const TM* Y, int x16, TM* P, const Decays<C>& d, float scale,
+template <int PL, int C, int DX, int NP, bool REV, int WAVES>
+__device__ __forceinline__ void scores(const bf16* X, const bf16* Y, int x16, bf16* P, const Decays<C>& d, float scale,
                                        int wave) {
   const int l = fresh_lane();
   x16 = fresh(x16);
   constexpr int N = (kTiles<C> + WAVES - 1) / WAVES;
-  ScoreFrags<TM, DX> f[2];
+  constexpr bool AHEAD = PL == 1;  // the next tile's reads before this one's product
+  ScoreFrags<PL, C, DX> f[AHEAD ? 2 : 1];
   int rt, ct;
   tile_of<C, REV>(wave, rt, ct);
   if (wave < kTiles<C>) f[0].read(X, Y, x16, rt, ct);
@@ -112,16 +133,16 @@ __device__ __forceinline__ void scores(const TM* X, const TM* Y, int x16, TM* P,
     const int i = wave + j * WAVES;
     if (i >= kTiles<C>) break;
     int rn = 0, cn = 0;
-    if (i + WAVES < kTiles<C>) {  // the next tile's reads before this one's product
-      tile_of<C, REV>(i + WAVES, rn, cn);
-      f[(j + 1) & 1].read(X, Y, x16, rn, cn);
-    }
+    const bool more = i + WAVES < kTiles<C>;
+    if (more) tile_of<C, REV>(i + WAVES, rn, cn);
+    if (AHEAD && more) f[(j + 1) & 1].read(X, Y, x16, rn, cn);
     const f4v dec = decay_tile<C, REV>(d, rt, ct, l);
     step_fence();
-    f4v acc = f[j & 1].product();
+    f4v acc = f[AHEAD ? j & 1 : 0].product();
+    if (!AHEAD && more) f[0].read(X, Y, x16, rn, cn);
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc[e] = dec[e] != 0.f ? acc[e] * (dec[e] * scale) : 0.f;
-    put_tile<TM, C, NP>(P, acc, rt, ct, l);
+    put_tile<C, NP>(P, acc, rt, ct, l);
     rt = rn;
     ct = cn;
   }
@@ -149,36 +170,39 @@ __device__ __forceinline__ void interleave() {
 }
 
 // acc[rt] = rows rt*32 .. + 31 of X times the state, transposed: lane l has row
-// l % 32, register 4 a + i the wave's column 8 a + 4 (l / 32) + i. Reads run two
-// steps ahead, and a step splits the next one's state between its products.
-template <class TM, int C, int DX, int NS>
-__device__ __forceinline__ void from_state(const TM* X, int x32, const f16v (&S)[DX / 32], f16v (&acc)[C / 32]) {
+// l % 32, register 4 a + i the wave's column 8 a + 4 (l / 32) + i. Steps go over
+// the state's rows and, inside, X's planes; reads run two steps ahead, and a step
+// splits the next one's state between its own products.
+template <int PL, int C, int DX, int NS>
+__device__ __forceinline__ void from_state(const bf16* X, int x32, const f16v (&S)[DX / 32], f16v (&acc)[C / 32]) {
   constexpr int RT = C / 32, N = DX / 16;
   x32 = fresh(x32);
 #pragma unroll
   for (int rt = 0; rt < RT; ++rt)
 #pragma unroll
     for (int r = 0; r < 16; ++r) acc[rt][r] = 0.f;
-  typename Math<TM>::Frag x[3][RT], piece[2][NS];
+  bf8 x[3][RT], piece[2][NS];
+  const auto read = [&](int i) {
 #pragma unroll
-  for (int s = 0; s < 2; ++s)
+    for (int rt = 0; rt < RT; ++rt)
+      x[i % 3][rt] = row_frag<DX>(X + (i % PL) * C * DX, x32, rt * 32, i / PL * 16);
+  };
+  read(0);
+  read(1);
+  split8<NS>(state8<DX / 32>(S, 0), piece[0]);
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) x[s][rt] = row_frag<TM, DX>(X, x32, rt * 32, s * 16);
-  split8<TM, NS>(state8<DX / 32>(S, 0), piece[0]);
-#pragma unroll
-  for (int s = 0; s < N; ++s) {
+  for (int i = 0; i < N * PL; ++i) {
+    const int s = i / PL, pl = i % PL;
     step_fence();
-    if (s + 2 < N) {
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) x[(s + 2) % 3][rt] = row_frag<TM, DX>(X, x32, rt * 32, (s + 2) * 16);
-    }
+    if (i + 2 < N * PL) read(i + 2);
     step_fence();
 #pragma unroll
     for (int p = 0; p < NS; ++p)
+      if (pl + p < NS)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt) acc[rt] = Math<TM>::mma32(piece[s & 1][p], x[s % 3][rt], acc[rt]);
-    if (s + 1 < N) split8<TM, NS>(state8<DX / 32>(S, s + 1), piece[(s + 1) & 1]);
-    if constexpr (sizeof(TM) == 2) interleave<NS * RT, 7>();
+        for (int rt = 0; rt < RT; ++rt) acc[rt] = mma32(piece[s & 1][p], x[i % 3][rt], acc[rt]);
+    if (pl == 0 && s + 1 < N) split8<NS>(state8<DX / 32>(S, s + 1), piece[(s + 1) & 1]);
+    interleave<NS * RT, 7>();
   }
   step_fence();
 }
@@ -201,38 +225,42 @@ __device__ __forceinline__ void scale_state(f16v (&S)[NT], float f) {
     for (int r = 0; r < 16; ++r) S[t][r] *= f;
 }
 // The wave's 32 columns of Z for one 16-step js, times f, in pieces.
-template <class TM, int NS>
-__device__ __forceinline__ void weigh(typename Math<TM>::Frag z, const float* f, int js,
-                                      typename Math<TM>::Frag (&piece)[NS]) {
+template <int PL, int NS>
+__device__ __forceinline__ void weigh(const bf8 (&z)[PL], const float* f, int js, bf8 (&piece)[NS]) {
   const int h = lane_id() >> 5;
   const f4v fa = *(const f4v*)(f + js * 16 + 8 * h), fb = *(const f4v*)(f + js * 16 + 8 * h + 4);
-  f8v w = Math<TM>::widen(z);
+  f8v w = widen(z[PL - 1]);
+#pragma unroll
+  for (int p = PL - 2; p >= 0; --p) w += widen(z[p]);  // exact, smallest first
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     w[i] *= fa[i];
     w[4 + i] *= fb[i];
   }
-  split8<TM, NS>(w, piece);
+  split8<NS>(w, piece);
 }
 // S = e^{b_C} S + Y^T (in Z) and, with P, acc += P Z on the same reads of Z.
-template <class TM, int C, int DX, int DZ, int NP, int NS, bool REV>
-__device__ __forceinline__ void within_chunk(const TM* Y, const TM* Z, const TM* P, const Decays<C>& d,
-                                             const LaneOffsets<TM, C, DX, DZ>& at, f16v (&S)[DX / 32],
+template <int PL, int C, int DX, int DZ, int NP, bool REV>
+__device__ __forceinline__ void within_chunk(const bf16* Y, const bf16* Z, const bf16* P, const Decays<C>& d,
+                                             const LaneOffsets<C, DX, DZ>& at, f16v (&S)[DX / 32],
                                              f16v (&acc)[C / 32]) {
-  typedef typename Math<TM>::Frag Frag;
-  constexpr int RT = C / 32, KP = NP > 0 ? NP : 1, JS = C / 16;
-  Frag z[2], y[DX / 32], pf[RT][KP], piece[2][NS];
+  constexpr int RT = C / 32, KP = NP > 0 ? NP : 1, JS = C / 16, NS = kPiecesZ;
+  bf8 z[2][PL], y[DX / 32], pf[RT][KP], piece[2][NS];
   const int oy = fresh(at.y), oz = fresh(at.z), op = fresh(at.p);
   const auto inside = [](int rt, int js) { return REV ? js * 16 >= rt * 32 : js * 16 < rt * 32 + 32; };
-  const auto read_y = [&](int js) {
+  const auto read_y = [&](int js, int pl) {
 #pragma unroll
-    for (int t = 0; t < DX / 32; ++t) y[t] = col_frag<TM, DX>(Y, oy, js * 16, t * 32);
+    for (int t = 0; t < DX / 32; ++t) y[t] = col_frag<DX>(Y + pl * C * DX, oy, js * 16, t * 32);
   };
-  z[0] = col_frag<TM, DZ>(Z, oz, 0, 0);
-  read_y(0);
-  if (JS > 1) z[1] = col_frag<TM, DZ>(Z, oz, 16, 0);
+  const auto read_z = [&](int js) {
+#pragma unroll
+    for (int pl = 0; pl < PL; ++pl) z[js & 1][pl] = col_frag<DZ>(Z + pl * C * DZ, oz, js * 16, 0);
+  };
+  read_z(0);
+  read_y(0, 0);
+  read_z(1);
   scale_state<DX / 32>(S, d.all);
-  weigh<TM, NS>(z[0], d.in, 0, piece[0]);
+  weigh<PL, NS>(z[0], d.in, 0, piece[0]);
 #pragma unroll
   for (int js = 0; js < JS; ++js) {
     step_fence();
@@ -242,23 +270,31 @@ __device__ __forceinline__ void within_chunk(const TM* Y, const TM* Z, const TM*
     for (int rt = 0; rt < RT; ++rt)
       if (inside(rt, js))
 #pragma unroll
-        for (int p = 0; p < NP; ++p) pf[rt][p] = row_frag<TM, C>(P + p * C * C, op, rt * 32, js * 16);
-    step_fence();
+        for (int p = 0; p < NP; ++p) pf[rt][p] = row_frag<C>(P + p * C * C, op, rt * 32, js * 16);
 #pragma unroll
-    for (int p = 0; p < NS; ++p)
+    for (int pl = 0; pl < PL; ++pl) {
+      step_fence();
 #pragma unroll
-      for (int t = 0; t < DX / 32; ++t) S[t] = Math<TM>::mma32(y[t], piece[js & 1][p], S[t]);
-    if (js + 1 < JS) weigh<TM, NS>(z[(js + 1) & 1], d.in, js + 1, piece[(js + 1) & 1]);
-    if constexpr (sizeof(TM) == 2) interleave<NS * (DX / 32), 6>();
-    step_fence();
-    if (js + 1 < JS) read_y(js + 1);
+      for (int p = 0; p < NS; ++p)
+        if (pl + p < NS)
+#pragma unroll
+          for (int t = 0; t < DX / 32; ++t) S[t] = mma32(y[t], piece[js & 1][p], S[t]);
+      if (pl == 0 && js + 1 < JS) weigh<PL, NS>(z[(js + 1) & 1], d.in, js + 1, piece[(js + 1) & 1]);
+      interleave<NS * (DX / 32), 6>();
+      step_fence();
+      if (pl + 1 < PL) read_y(js, pl + 1);
+      else if (js + 1 < JS) read_y(js + 1, 0);
+    }
     step_fence();
 #pragma unroll
     for (int p = 0; p < NP; ++p)
 #pragma unroll
-      for (int rt = 0; rt < RT; ++rt)
-        if (inside(rt, js)) acc[rt] = Math<TM>::mma32(z[js & 1], pf[rt][p], acc[rt]);
-    if (js + 2 < JS) z[js & 1] = col_frag<TM, DZ>(Z, oz, (js + 2) * 16, 0);
+      for (int pl = 0; pl < PL; ++pl)
+        if (pl + p < NP || PL == 1)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+            if (inside(rt, js)) acc[rt] = mma32(z[js & 1][pl], pf[rt][p], acc[rt]);
+    if (js + 2 < JS) read_z(js + 2);
   }
   step_fence();
 }
@@ -326,16 +362,18 @@ __device__ __forceinline__ float sum16(float x) {  // over the 16 lanes of a DPP
   return ror_add<0x121>(ror_add<0x122>(ror_add<0x124>(ror_add<0x128>(x))));
 }
 // Sums over the wave's 32 columns of acc times the rows of a tile, to dst[C].
-template <class TM, int C, int D>
-__device__ __forceinline__ void row_dots(const f16v (&acc)[C / 32], const TM* tile, int z0, float* dst) {
-  typedef TM four __attribute__((ext_vector_type(4)));
-  const int l = fresh_lane(), off = cell_at<TM, D>(l & 31, z0 + ((l >> 5) << 2));
+template <int PL, int C, int D>
+__device__ __forceinline__ void row_dots(const f16v (&acc)[C / 32], const bf16* tile, int z0, float* dst) {
+  const int l = fresh_lane(), off = cell_at<bf16, D>(l & 31, z0 + ((l >> 5) << 2));
 #pragma unroll
   for (int rt = 0; rt < C / 32; ++rt) {
     float s = 0.f;
 #pragma unroll
     for (int a = 0; a < 4; ++a) {
-      const f4v w = __builtin_convertvector(*(const four*)(tile + moved<TM, D>(off, rt * 32, a * 8 / kUnit<TM>)), f4v);
+      const bf16* at = tile + moved<bf16, D>(off, rt * 32, a);
+      f4v w = __builtin_convertvector(*(const bf4*)(at + (PL - 1) * C * D), f4v);
+#pragma unroll
+      for (int p = PL - 2; p >= 0; --p) w += __builtin_convertvector(*(const bf4*)(at + p * C * D), f4v);
 #pragma unroll
       for (int i = 0; i < 4; ++i) s += acc[rt][a * 4 + i] * w[i];
     }
@@ -459,12 +497,12 @@ __device__ __forceinline__ float load_gate(const float* g, int64_t st, int t0, i
 // Decay over a span and the state it adds, from a zero state: REV runs the
 // adjoint's recurrence. Not needed for the span that ends a sequence (REV: that
 // starts it), whose state nothing reads.
-template <class TIn, class TM, int DX, int NW, bool REV>
+template <class TIn, int DX, int NW, bool REV>
 __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, const Heads y, const Heads z, float sz,
-                                                         float* states, float* totals) {
-  constexpr int C = kChunk<TM>, DZ = NW * 32, NT = NW * 64;
-  __shared__ __align__(16) TM Y[C * DX];
-  __shared__ __align__(16) TM Z[C * DZ];
+                                                            float* states, float* totals) {
+  constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, DZ = NW * 32, NT = NW * 64;
+  __shared__ __align__(16) bf16 Y[PL * C * DX];
+  __shared__ __align__(16) bf16 Z[PL * C * DZ];
   __shared__ __align__(16) Decays<C> dec;
   const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
@@ -484,7 +522,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
   TileRegs<TIn, C, DZ, NT> rz[2];
   float rg[2] = {0.f, 0.f};
   double total = 0.0;
-  const LaneOffsets<TM, C, DX, DZ> at(z0);
+  const LaneOffsets<C, DX, DZ> at(z0);
   f16v none[C / 32];
   const auto fetch = [&](int i, int s) {
     const int c = REV ? nc - 1 - i : i, t = c * C;
@@ -498,7 +536,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
     if (wave == 0) total += write_decays<C, REV>(dec, rg[s], sz);
     __syncthreads();
     if (i + 2 < nc) fetch(i + 2, s);
-    within_chunk<TM, C, DX, DZ, 0, kPiecesZ<TM>, REV>(Y, Z, nullptr, dec, at, S, none);
+    within_chunk<PL, C, DX, DZ, 0, REV>(Y, Z, nullptr, dec, at, S, none);
     __syncthreads();
   };
   fetch(0, 0);

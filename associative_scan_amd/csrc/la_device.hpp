@@ -23,8 +23,9 @@
 namespace mscan {
 namespace la {
 
-typedef __bf16 bf8 __attribute__((ext_vector_type(8)));
-typedef __bf16 bf4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16;
+typedef bf16 bf8 __attribute__((ext_vector_type(8)));
+typedef bf16 bf4 __attribute__((ext_vector_type(4)));
 typedef short s4v __attribute__((ext_vector_type(4)));
 typedef float f4v __attribute__((ext_vector_type(4)));
 typedef float f8v __attribute__((ext_vector_type(8)));
@@ -61,46 +62,22 @@ __device__ __forceinline__ void settle() { __builtin_amdgcn_s_waitcnt(0); }
 __device__ __forceinline__ void step_fence() { __builtin_amdgcn_sched_barrier(0); }
 
 // ---------------------------------------------------------------------------
-// matrix-core fragments
+// numbers as sums of bf16
 //
-// A fragment holds 8 values per lane of an operand's contraction axis: lanes l
-// and l + 32 of a 32-wide tile take entries 8 h .. 8 h + 7, h = l / 32, of a
-// 16-step. An accumulator of a state holds, in 8 consecutive registers, rows
-// 8 e + 4 h + i (e < 2, i < 4) of 16; the state's rows are numbered so that these
-// are its entries 8 h + 4 e + i (state_row), which makes a state kept in
-// accumulators an operand without a move between lanes. fp32 math issues eight
-// products of one value per lane in place of one 16-bit product of eight.
+// All products run on the bf16 matrix cores, whose sums are fp32. A value of more
+// than 8 bits is a sum of bf16 pieces, each the rounding of what the ones before
+// it left: an fp16 input is exactly two, an fp32 one three (both below 2^127 2),
+// and a product of two such sums is the products of their pieces, the ones below
+// 2^-24 of it left out. Three pieces cost six products of 32 cycles for 16 steps
+// of a 32 x 32 tile; the fp32 matrix instructions take 512 cycles for them.
 // ---------------------------------------------------------------------------
-template <class TM>
-struct Math;
-
+// Pieces of an input: planes of its tiles.
+template <class T>
+constexpr int kPlanes = 1;
 template <>
-struct Math<__bf16> {
-  typedef bf8 Frag;
-  static __device__ __forceinline__ f16v mma32(Frag a, Frag b, f16v c) {
-    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ f4v mma16(Frag a, Frag b, f4v c) {
-    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
-  }
-  static __device__ __forceinline__ f8v widen(Frag f) { return __builtin_convertvector(f, f8v); }
-};
-
+inline constexpr int kPlanes<_Float16> = 2;
 template <>
-struct Math<float> {
-  typedef f8v Frag;
-  static __device__ __forceinline__ f16v mma32(Frag a, Frag b, f16v c) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], c, 0, 0, 0);
-    return c;
-  }
-  static __device__ __forceinline__ f4v mma16(Frag a, Frag b, f4v c) {
-#pragma unroll
-    for (int e = 0; e < 8; ++e) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], c, 0, 0, 0);
-    return c;
-  }
-  static __device__ __forceinline__ f8v widen(Frag f) { return f; }
-};
+inline constexpr int kPlanes<float> = 3;
 
 // Two fp32 values rounded to bf16 in one register. As an instruction of its own:
 // the compiler otherwise converts a value twice, once for the pair and once for
@@ -110,9 +87,8 @@ __device__ __forceinline__ uint32_t bf16_pair(float a, float b) {
   asm("v_cvt_pk_bf16_f32 %0, %1, %2" : "=v"(w) : "v"(a), "v"(b));
   return w;
 }
-// x as a sum of N fragments: bf16 pieces of 8 bits each, every piece the
-// rounding of what the ones before it left (N = 2: off by 2^-18 of x at most,
-// N = 3: exact but for fp32's own last bits); fp32 math takes x whole.
+// x as N pieces (N = 2: off by 2^-18 of x at most, N = 3: exact but for fp32's
+// own last bits), x left with what they leave.
 template <int N, int E>
 __device__ __forceinline__ void split_pairs(float (&x)[E], uint32_t (&out)[N][E / 2]) {
 #pragma unroll
@@ -127,41 +103,41 @@ __device__ __forceinline__ void split_pairs(float (&x)[E], uint32_t (&out)[N][E 
       }
     }
 }
-template <class TM, int N>
-__device__ __forceinline__ void split8(f8v x, typename Math<TM>::Frag (&out)[N]) {
-  if constexpr (sizeof(TM) == 4) {
-    out[0] = x;
-  } else {
-    float v[8];
-    uint32_t w[N][4];
+template <int N>
+__device__ __forceinline__ void split8(f8v x, bf8 (&out)[N]) {
+  float v[8];
+  uint32_t w[N][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = x[i];
-    split_pairs<N, 8>(v, w);
+  for (int i = 0; i < 8; ++i) v[i] = x[i];
+  split_pairs<N, 8>(v, w);
 #pragma unroll
-    for (int p = 0; p < N; ++p) out[p] = __builtin_bit_cast(bf8, u4v{w[p][0], w[p][1], w[p][2], w[p][3]});
-  }
+  for (int p = 0; p < N; ++p) out[p] = __builtin_bit_cast(bf8, u4v{w[p][0], w[p][1], w[p][2], w[p][3]});
 }
-template <class TM>
-struct Four;  // 4 consecutive elements of a tile row
-template <>
-struct Four<__bf16> {
-  typedef u2v type;
-};
-template <>
-struct Four<float> {
-  typedef f4v type;
-};
-template <class TM, int N>
-__device__ __forceinline__ void split4(f4v x, typename Four<TM>::type (&out)[N]) {
-  if constexpr (sizeof(TM) == 4) {
-    out[0] = x;
-  } else {
-    float v[4] = {x[0], x[1], x[2], x[3]};
-    uint32_t w[N][2];
-    split_pairs<N, 4>(v, w);
+template <int N>
+__device__ __forceinline__ void split4(f4v x, u2v (&out)[N]) {
+  float v[4] = {x[0], x[1], x[2], x[3]};
+  uint32_t w[N][2];
+  split_pairs<N, 4>(v, w);
 #pragma unroll
-    for (int p = 0; p < N; ++p) out[p] = u2v{w[p][0], w[p][1]};
-  }
+  for (int p = 0; p < N; ++p) out[p] = u2v{w[p][0], w[p][1]};
+}
+__device__ __forceinline__ f8v widen(bf8 f) { return __builtin_convertvector(f, f8v); }
+
+// ---------------------------------------------------------------------------
+// matrix-core fragments
+//
+// A fragment holds 8 values per lane of an operand's contraction axis: lanes l
+// and l + 32 of a 32-wide tile take entries 8 h .. 8 h + 7, h = l / 32, of a
+// 16-step. An accumulator of a state holds, in 8 consecutive registers, rows
+// 8 e + 4 h + i (e < 2, i < 4) of 16; the state's rows are numbered so that these
+// are its entries 8 h + 4 e + i (state_row), which makes a state kept in
+// accumulators an operand without a move between lanes.
+// ---------------------------------------------------------------------------
+__device__ __forceinline__ f16v mma32(bf8 a, bf8 b, f16v c) {
+  return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f4v mma16(bf8 a, bf8 b, f4v c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
 }
 
 // ---------------------------------------------------------------------------
@@ -180,7 +156,8 @@ constexpr int kUnit = 16 / (int)sizeof(TM);  // elements of a unit
 template <class TM, int D>
 __device__ __forceinline__ constexpr int swizzle(int row) {
   constexpr int U = D / kUnit<TM>;
-  static_assert(U == 8 || U == 16 || U == 32, "tile width");
+  static_assert(U == 4 || U == 8 || U == 16 || U == 32, "tile width");
+  if constexpr (U == 4) return (row >> 2) & 3;
   if constexpr (U == 8) return (((row >> 1) & 1) << 2) | ((row >> 2) & 3);
   return ((row & 3) << 2) | ((row >> 2) & 3);
 }
@@ -201,21 +178,14 @@ __device__ __forceinline__ int cell_at(int row, int col) {
 // Row fragments: R-wide tiles (R = 32 or 16), contraction axis along the rows.
 // Lane offset, and the fragment of rows row0 (a multiple of R) + l % R, entries
 // k0 + 8 (l / R) .. + 7, k0 a multiple of the step (16 or 32).
-template <class TM, int D, int R>
+template <int D, int R>
 __device__ __forceinline__ int row_lane() {
   const int l = lane_id();
-  return unit_at<TM, D>(l % R, l / R * (8 / kUnit<TM>));
+  return unit_at<bf16, D>(l % R, l / R);
 }
-template <class TM, int D>
-__device__ __forceinline__ typename Math<TM>::Frag row_frag(const TM* tile, int off, int row0, int k0) {
-  const int u = k0 / kUnit<TM>;
-  if constexpr (sizeof(TM) == 2) {
-    return *(const bf8*)(tile + moved<TM, D>(off, row0, u));
-  } else {
-    const f4v a = *(const f4v*)(tile + moved<TM, D>(off, row0, u));
-    const f4v b = *(const f4v*)(tile + moved<TM, D>(off, row0, u + 1));
-    return __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7);
-  }
+template <int D>
+__device__ __forceinline__ bf8 row_frag(const bf16* tile, int off, int row0, int k0) {
+  return *(const bf8*)(tile + moved<bf16, D>(off, row0, k0 / 8));
 }
 // Entry of a state's 32 rows that row m of its accumulators holds: bits 2 and 3
 // change places.
@@ -223,32 +193,21 @@ __device__ __forceinline__ constexpr int state_row(int m) { return (m & ~12) | (
 
 // Column fragments: 32-wide tiles, contraction axis down the rows row0 + 8 h ..
 // + 7, row0 a multiple of 16. Columns col0 (a multiple of 32) + l % 32, or, as
-// rows of a state (STATE), col0 + state_row(l % 32).
-template <class TM, int D, bool STATE>
+// rows of a state (STATE), col0 + state_row(l % 32). A transposing read: each 16
+// lanes read 4 rows x 16 columns, lane i of them 8 bytes of row i / 4, and get
+// column i of the four rows.
+template <int D, bool STATE>
 __device__ __forceinline__ int col_lane() {
   const int l = lane_id(), h = l >> 5;
-  if constexpr (sizeof(TM) == 2) {
-    // a transposing read: each 16 lanes read 4 rows x 16 columns, lane i of
-    // them 8 bytes of row i / 4, and get column i of the four rows
-    const int four = STATE ? ((l & 1) << 1) | ((l & 2) >> 1) : l & 3;  // of the 16 columns
-    return unit_at<TM, D>(8 * h + ((l & 15) >> 2), ((l >> 4) & 1) * 2 + (four >> 1)) + (four & 1) * 4;
-  } else {
-    return cell_at<TM, D>(8 * h, STATE ? state_row(l & 31) : l & 31);
-  }
+  const int four = STATE ? ((l & 1) << 1) | ((l & 2) >> 1) : l & 3;  // of the 16 columns
+  return unit_at<bf16, D>(8 * h + ((l & 15) >> 2), ((l >> 4) & 1) * 2 + (four >> 1)) + (four & 1) * 4;
 }
-template <class TM, int D>
-__device__ __forceinline__ typename Math<TM>::Frag col_frag(const TM* tile, int off, int row0, int col0) {
-  if constexpr (sizeof(TM) == 2) {
-    typedef __attribute__((address_space(3))) s4v* lds4;
-    const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + moved<TM, D>(off, row0, col0 / 8)));
-    const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + moved<TM, D>(off, row0 + 4, col0 / 8)));
-    return __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
-  } else {
-    f8v f;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) f[e] = tile[moved<TM, D>(off, row0 + e, col0 / 4)];
-    return f;
-  }
+template <int D>
+__device__ __forceinline__ bf8 col_frag(const bf16* tile, int off, int row0, int col0) {
+  typedef __attribute__((address_space(3))) s4v* lds4;
+  const s4v a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + moved<bf16, D>(off, row0, col0 / 8)));
+  const s4v b = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4)(tile + moved<bf16, D>(off, row0 + 4, col0 / 8)));
+  return __builtin_bit_cast(bf8, __builtin_shufflevector(a, b, 0, 1, 2, 3, 4, 5, 6, 7));
 }
 
 // ---------------------------------------------------------------------------
@@ -296,25 +255,28 @@ struct TileRegs {
       off += step;
     }
   }
-  template <class TM>
-  __device__ __forceinline__ void store(TM* tile) const {
+  // as kPlanes<TIn> tiles of C x D, one behind the other
+  __device__ __forceinline__ void store(bf16* tile) const {
+    constexpr int PL = kPlanes<TIn>;
     const unsigned tid = fresh_thread();
-    const int off = unit_at<TM, D>((int)(tid / (D / 8)), (int)(tid % (D / 8)) * (8 / kUnit<TM>));
+    const int off = unit_at<bf16, D>((int)(tid / (D / 8)), (int)(tid % (D / 8)));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      TM* a = tile + moved<TM, D>(off, i * STEP, 0);
-      if constexpr (sizeof(TM) == 2) {
-        *(u4v*)a = r[i].w[0];
+      bf16* at = tile + moved<bf16, D>(off, i * STEP, 0);
+      if constexpr (PL == 1) {
+        *(u4v*)at = r[i].w[0];
       } else {
-        TM* b = tile + moved<TM, D>(off, i * STEP, 1);
-        if constexpr (sizeof(TIn) == 4) {
-          *(u4v*)a = r[i].w[0];
-          *(u4v*)b = r[i].w[1];
-        } else {  // 16-bit input, fp32 math: widened exactly
-          const f8v f = __builtin_convertvector(__builtin_bit_cast(h8, r[i].w[0]), f8v);
-          *(f4v*)a = __builtin_shufflevector(f, f, 0, 1, 2, 3);
-          *(f4v*)b = __builtin_shufflevector(f, f, 4, 5, 6, 7);
+        f8v x;
+        if constexpr (PL == 2) {
+          x = __builtin_convertvector(__builtin_bit_cast(h8, r[i].w[0]), f8v);
+        } else {
+          x = __builtin_shufflevector(__builtin_bit_cast(f4v, r[i].w[0]), __builtin_bit_cast(f4v, r[i].w[1]), 0, 1, 2, 3,
+                                      4, 5, 6, 7);
         }
+        bf8 piece[PL];
+        split8<PL>(x, piece);
+#pragma unroll
+        for (int p = 0; p < PL; ++p) *(bf8*)(at + p * C * D) = piece[p];
       }
     }
   }

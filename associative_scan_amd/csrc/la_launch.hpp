@@ -30,7 +30,7 @@ struct LaProblem {
 };
 
 // Steps per span, for LaProblem::span; sets spans and slots too.
-void plan(LaProblem& p);
+void plan(LaProblem& p, int dtype, bool backward);
 
 // The states between spans: what each span adds (see k_span_states), and from
 // these the states at the spans' starts (rev: the adjoint's at their ends).

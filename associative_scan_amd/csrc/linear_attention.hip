@@ -12,13 +12,13 @@
 namespace mscan {
 namespace la {
 
-template <class TIn, class TM, int DX, int NW>
+template <class TIn, int DX, int NW>
 __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
-  constexpr int C = kChunk<TM>, DZ = NW * 32, NT = NW * 64, NP = kPiecesP<TM>;
-  __shared__ __align__(16) TM Q[C * (DX > DZ ? DX : DZ)];  // and then the chunk's outputs
-  __shared__ __align__(16) TM K[C * DX];
-  __shared__ __align__(16) TM V[C * DZ];
-  __shared__ __align__(16) TM P[NP * C * C];
+  constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, DZ = NW * 32, NT = NW * 64, NP = kPiecesP<TIn>;
+  __shared__ __align__(16) bf16 Q[PL * C * (DX > DZ ? DX : DZ)];  // and then the chunk's outputs
+  __shared__ __align__(16) bf16 K[PL * C * DX];
+  __shared__ __align__(16) bf16 V[PL * C * DZ];
+  __shared__ __align__(16) bf16 P[NP * C * C];
   __shared__ __align__(16) Decays<C> dec[2];
   const LaProblem& pr = a.pr;
   const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
@@ -51,7 +51,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   };
   const auto fetch_k = [&](int t) { rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t); };
   const auto fetch_v = [&](int t) { rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t); };
-  const LaneOffsets<TM, C, DX, DZ> at(z0);
+  const LaneOffsets<C, DX, DZ> at(z0);
   if (sp.n > 0) {
     fetch_q(0);
     fetch_k(0);
@@ -66,20 +66,20 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   for (int t = 0, cur = 0; t < sp.n; t += C, cur ^= 1) {
     const bool more = t + C < sp.n;
     if (more) fetch_q(t + C);
-    scores<TM, C, DX, NP, false, NW>(Q, K, at.x16, P, dec[cur], pr.scale, wave);
+    scores<PL, C, DX, NP, false, NW>(Q, K, at.x16, P, dec[cur], pr.scale, wave);
     if (more) fetch_k(t + C);
     f16v acc[C / 32];
-    from_state<TM, C, DX, kPiecesX<TM>>(Q, at.x32, S, acc);
+    from_state<PL, C, DX, kPiecesS<TIn, false>>(Q, at.x32, S, acc);
     if (more) fetch_v(t + C);
     scale_rows<C>(acc, dec[cur].out);
     __syncthreads();
-    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(K, V, P, dec[cur], at, S, acc);
+    within_chunk<PL, C, DX, DZ, NP, false>(K, V, P, dec[cur], at, S, acc);
     if (more && wave == NW - 1) write_decays<C, false>(dec[cur ^ 1], rg, pr.scale);
     rows_to_lds<TIn, C, DZ>(acc, (TIn*)Q, z0);
     __syncthreads();
     OutRegs<TIn, C, DZ, NT> out;
     out.take((const TIn*)Q);
-    if constexpr (DX != DZ || sizeof(TIn) != sizeof(TM)) __syncthreads();
+    if constexpr (DX != DZ || PL != 1) __syncthreads();
     if (more) {
       rq.store(Q);
       rk.store(K);
@@ -149,19 +149,21 @@ hipError_t launch_join(const LaProblem& p, bool rev, const float* outer, float* 
 
 // Steps per span. A workgroup per head and sequence needs no second pass over
 // k and v, but fills the card only with many heads and sequences; with fewer the
-// time axis is cut. What a cut costs, in steps of the main pass (64 of them take
-// about 5 us on a CU of their own, 8 us where two workgroups share one): its spans
-// one after the other in as many rounds as the card's 512 places ask for, 0.45 of
-// that for the pass that gives the spans' own states, a round's start, and about
-// two chunks for the join and the launches.
-void plan(LaProblem& p) {
+// time axis is cut. What a cut costs, in steps of the main pass: its spans one
+// after the other in as many rounds as the card's 512 places ask for (a workgroup
+// with a CU of its own runs faster, 5 us for 64 bf16 steps against 8 us where two
+// share one), a round's start, the pass that gives the spans' own states (0.45 of
+// the forward kernel's time, 0.3 of the backward's), and the joins and launches,
+// some 10 us, which are fewer steps the longer a step takes.
+void plan(LaProblem& p, int dtype, bool backward) {
   const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H;
+  const double states = backward ? 1.3 : 1.45, fixed = (dtype == 1 ? 128 : 80) * (backward ? 0.6 : 1.0);
   const auto cost = [&](int64_t span) {
     const int64_t n = (p.T + span - 1) / span, blocks = n * rows;
     const int64_t rounds = (blocks + 511) / 512;
     const double step = blocks <= 256 ? 0.62 : 1.0;
     const double run = rounds * step * ((double)(span < p.T ? span : p.T) + 48);
-    return n == 1 ? run : 1.45 * run + 128 + 3.0 * n;
+    return n == 1 ? run : states * run + fixed + 3.0 * n;
   };
   int64_t best = (p.T + 63) / 64 * 64;
   double least = cost(best);
@@ -187,48 +189,48 @@ void plan(LaProblem& p) {
   }
 }
 
-template <class TIn, class TM, int DX, int NW>
+template <class TIn, int DX, int NW>
 static hipError_t states_dims(const LaProblem& p, bool rev, const Heads& y, const Heads& z, float sz, float* states,
                               float* totals, hipStream_t st) {
   const unsigned blocks = (unsigned)((int64_t)p.slots * p.H);
   if (rev)
-    hipLaunchKernelGGL((k_span_states<TIn, TM, DX, NW, true>), dim3(blocks), dim3(NW * 64), 0, st, p, y, z, sz, states,
+    hipLaunchKernelGGL((k_span_states<TIn, DX, NW, true>), dim3(blocks), dim3(NW * 64), 0, st, p, y, z, sz, states,
                        totals);
   else
-    hipLaunchKernelGGL((k_span_states<TIn, TM, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, p, y, z, sz,
+    hipLaunchKernelGGL((k_span_states<TIn, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, p, y, z, sz,
                        states, totals);
   return hipGetLastError();
 }
-template <class TIn, class TM>
+template <class TIn>
 static hipError_t states_type(const LaProblem& p, bool rev, const Heads& y, const Heads& z, float sz, float* states,
                               float* totals, hipStream_t st) {
   if (p.Dk <= 64)
-    return p.Dv <= 64 ? states_dims<TIn, TM, 64, 2>(p, rev, y, z, sz, states, totals, st)
-                      : states_dims<TIn, TM, 64, 4>(p, rev, y, z, sz, states, totals, st);
-  return p.Dv <= 64 ? states_dims<TIn, TM, 128, 2>(p, rev, y, z, sz, states, totals, st)
-                    : states_dims<TIn, TM, 128, 4>(p, rev, y, z, sz, states, totals, st);
+    return p.Dv <= 64 ? states_dims<TIn, 64, 2>(p, rev, y, z, sz, states, totals, st)
+                      : states_dims<TIn, 64, 4>(p, rev, y, z, sz, states, totals, st);
+  return p.Dv <= 64 ? states_dims<TIn, 128, 2>(p, rev, y, z, sz, states, totals, st)
+                    : states_dims<TIn, 128, 4>(p, rev, y, z, sz, states, totals, st);
 }
 hipError_t launch_span_states(const LaProblem& p, int dtype, bool rev, const Heads& y, const Heads& z, float sz,
                               float* states, float* totals, hipStream_t st) {
-  if (dtype == 0) return states_type<float, float>(p, rev, y, z, sz, states, totals, st);
-  if (dtype == 1) return states_type<__bf16, __bf16>(p, rev, y, z, sz, states, totals, st);
-  return states_type<_Float16, float>(p, rev, y, z, sz, states, totals, st);
+  if (dtype == 0) return states_type<float>(p, rev, y, z, sz, states, totals, st);
+  if (dtype == 1) return states_type<__bf16>(p, rev, y, z, sz, states, totals, st);
+  return states_type<_Float16>(p, rev, y, z, sz, states, totals, st);
 }
 
-template <class TIn, class TM, int DX, int NW>
+template <class TIn, int DX, int NW>
 static hipError_t fwd_dims(const FwdArgs& a, hipStream_t st) {
   const unsigned blocks = (unsigned)((int64_t)a.pr.slots * a.pr.H);
-  hipLaunchKernelGGL((k_attn_fwd<TIn, TM, DX, NW>), dim3(blocks), dim3(NW * 64), 0, st, a);
+  hipLaunchKernelGGL((k_attn_fwd<TIn, DX, NW>), dim3(blocks), dim3(NW * 64), 0, st, a);
   return hipGetLastError();
 }
 
-template <class TIn, class TM>
+template <class TIn>
 static hipError_t fwd_type(const FwdArgs& a, hipStream_t st) {
   const bool dk64 = a.pr.Dk <= 64, dv64 = a.pr.Dv <= 64;
-  if (dk64 && dv64) return fwd_dims<TIn, TM, 64, 2>(a, st);
-  if (dk64) return fwd_dims<TIn, TM, 64, 4>(a, st);
-  if (dv64) return fwd_dims<TIn, TM, 128, 2>(a, st);
-  return fwd_dims<TIn, TM, 128, 4>(a, st);
+  if (dk64 && dv64) return fwd_dims<TIn, 64, 2>(a, st);
+  if (dk64) return fwd_dims<TIn, 64, 4>(a, st);
+  if (dv64) return fwd_dims<TIn, 128, 2>(a, st);
+  return fwd_dims<TIn, 128, 4>(a, st);
 }
 
 hipError_t launch_fwd(const FwdArgs& a, int dtype, hipStream_t st) {
@@ -237,9 +239,9 @@ hipError_t launch_fwd(const FwdArgs& a, int dtype, hipStream_t st) {
     if (e != hipSuccess) return e;
     if ((e = launch_join(a.pr, false, a.h0, a.states, a.totals, st)) != hipSuccess) return e;
   }
-  if (dtype == 0) return fwd_type<float, float>(a, st);
-  if (dtype == 1) return fwd_type<__bf16, __bf16>(a, st);
-  return fwd_type<_Float16, float>(a, st);
+  if (dtype == 0) return fwd_type<float>(a, st);
+  if (dtype == 1) return fwd_type<__bf16>(a, st);
+  return fwd_type<_Float16>(a, st);
 }
 
 }  // namespace la

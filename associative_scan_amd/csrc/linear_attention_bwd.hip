@@ -29,13 +29,13 @@ __device__ __forceinline__ float block_sum(float x, float* lds) {
 }
 
 // DX: columns of do and v; NW waves of 32 columns of k and dq.
-template <class TIn, class TM, int DX, int NW, bool DG>
+template <class TIn, int DX, int NW, bool DG>
 __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
-  constexpr int C = kChunk<TM>, DZ = NW * 32, NT = NW * 64, NP = kPiecesP<TM>;
-  __shared__ __align__(16) TM O[C * (DX > DZ ? DX : DZ)];  // and then the chunk's dq
-  __shared__ __align__(16) TM V[C * DX];
-  __shared__ __align__(16) TM K[C * DZ];
-  __shared__ __align__(16) TM P[NP * C * C];
+  constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, DZ = NW * 32, NT = NW * 64, NP = kPiecesP<TIn>;
+  __shared__ __align__(16) bf16 O[PL * C * (DX > DZ ? DX : DZ)];  // and then the chunk's dq
+  __shared__ __align__(16) bf16 V[PL * C * DX];
+  __shared__ __align__(16) bf16 K[PL * C * DZ];
+  __shared__ __align__(16) bf16 P[NP * C * C];
   __shared__ __align__(16) Decays<C> dec[2];
   __shared__ float part[NW][C];
   const LaProblem& pr = a.pr;
@@ -73,7 +73,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   };
   const auto fetch_v = [&](int t) { rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t); };
   const auto fetch_k = [&](int t) { rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t); };
-  const LaneOffsets<TM, C, DX, DZ> at(z0);
+  const LaneOffsets<C, DX, DZ> at(z0);
   fetch_o(0);
   fetch_v(0);
   fetch_k(0);
@@ -87,9 +87,9 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
     const bool more = t + C < sp.n;
     RowRegs<TIn, C> rq;
     if constexpr (DG) rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t, z0);
-    scores<TM, C, DX, NP, false, NW>(O, V, at.x16, P, dec[cur], pr.scale, wave);
+    scores<PL, C, DX, NP, false, NW>(O, V, at.x16, P, dec[cur], pr.scale, wave);
     f16v acc[C / 32];
-    from_state<TM, C, DX, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(O, at.x32, S, acc);
+    from_state<PL, C, DX, kPiecesS<TIn, DG>>(O, at.x32, S, acc);
     scale_rows<C>(acc, dec[cur].out);
     if constexpr (DG) rq.dots(acc, part[wave]);
     if (more) fetch_o(t + C);
@@ -102,7 +102,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
         for (int w = 0; w < NW; ++w) s += part[w][tid];
         rows[row0 + (int64_t)(t + tid) * pr.H] = s;
       }
-    within_chunk<TM, C, DX, DZ, NP, kPiecesZ<TM>, false>(V, K, P, dec[cur], at, S, acc);
+    within_chunk<PL, C, DX, DZ, NP, false>(V, K, P, dec[cur], at, S, acc);
     if (more) fetch_k(t + C);
     const int64_t o = row0 * pr.Dk + (int64_t)t * ost;
     OutRegs<TIn, C, DZ, NT> out;
@@ -111,7 +111,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
     if (more && wave == NW - 1) write_decays<C, false>(dec[cur ^ 1], rg, pr.scale);
     __syncthreads();
     if (!shared) out.take((const TIn*)O);
-    if constexpr (DX != DZ || sizeof(TIn) != sizeof(TM)) __syncthreads();
+    if constexpr (DX != DZ || PL != 1) __syncthreads();
     if (more) {
       ro.store(O);
       rv.store(V);
@@ -137,14 +137,14 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
 }
 
 // dk and dv. D: columns of every tile; NW waves for dv, then NW for dk.
-template <class TIn, class TM, int D, bool DG>
+template <class TIn, int D, bool DG>
 __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
-  constexpr int C = kChunk<TM>, NW = D / 32, NT = NW * 128, NP = kPiecesP<TM>;
-  __shared__ __align__(16) TM Q[C * D];
-  __shared__ __align__(16) TM K[C * D];  // and then the chunk's dk
-  __shared__ __align__(16) TM V[C * D];  // and then the chunk's dv
-  __shared__ __align__(16) TM O[C * D];
-  __shared__ __align__(16) TM P[2][NP * C * C];
+  constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, NW = D / 32, NT = NW * 128, NP = kPiecesP<TIn>;
+  __shared__ __align__(16) bf16 Q[PL * C * D];
+  __shared__ __align__(16) bf16 K[PL * C * D];  // and then the chunk's dk
+  __shared__ __align__(16) bf16 V[PL * C * D];  // and then the chunk's dv
+  __shared__ __align__(16) bf16 O[PL * C * D];
+  __shared__ __align__(16) bf16 P[2][NP * C * C];
   __shared__ __align__(16) Decays<C> dec[2];
   __shared__ float part[NW][C];
   __shared__ float sums[kTiles<C>][2][16];
@@ -175,9 +175,9 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
   f16v S[NW];
   if (is_dk) load_state_t<D>(S, lam, pr.Dv, pr.Dv, pr.Dk, z0);
   else load_state<D>(S, lam, pr.Dv, 1, pr.Dk, pr.Dv, z0);
-  const TM* X = is_dk ? V : K;
-  const TM* Y = is_dk ? O : Q;
-  const TM* Z = is_dk ? Q : O;
+  const bf16* X = is_dk ? V : K;
+  const bf16* Y = is_dk ? O : Q;
+  const bf16* Z = is_dk ? Q : O;
   const TIn* qp = head_base<TIn>(a.q, sp.batch, sp.t0, h);
   const TIn* kp = head_base<TIn>(a.k, sp.batch, sp.t0, h);
   const TIn* vp = head_base<TIn>(a.v, sp.batch, sp.t0, h);
@@ -198,7 +198,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
     rv.store(V);
     ro.store(O);
   };
-  const LaneOffsets<TM, C, D, D> at(z0);
+  const LaneOffsets<C, D, D> at(z0);
   const int last = sp.n > 0 ? (sp.n - 1) / C * C : -C;
   if (last >= 0) {
     fetch_k(last);
@@ -219,11 +219,13 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
         int rt, ct;
         tile_of<C, true>(i, rt, ct);
         const f4v d = decay_tile<C, true>(dec[cur], rt, ct, l);
-        ScoreFrags<TM, D> fx, fy;
+        ScoreFrags<PL, C, D> fx, fy;
         fx.read(K, Q, at.x16, rt, ct);
-        fy.read(V, O, at.x16, rt, ct);
+        if (PL == 1) fy.read(V, O, at.x16, rt, ct);
         step_fence();
-        f4v x = fx.product(), y = fy.product();
+        f4v x = fx.product();
+        if (PL > 1) fy.read(V, O, at.x16, rt, ct);
+        f4v y = fy.product();
         float row[4], col = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -234,8 +236,8 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
           col += row[e];
           y[e] = d[e] != 0.f ? y[e] * f : 0.f;
         }
-        put_tile<TM, C, NP>(P[0], x, rt, ct, l);
-        put_tile<TM, C, NP>(P[1], y, rt, ct, l);
+        put_tile<C, NP>(P[0], x, rt, ct, l);
+        put_tile<C, NP>(P[1], y, rt, ct, l);
         if constexpr (DG) {
           col += __shfl_xor(col, 16);
           col += __shfl_xor(col, 32);
@@ -250,11 +252,11 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
     }
     if (more) fetch_q(t - C);
     f16v acc[C / 32];
-    from_state<TM, C, D, DG ? kPiecesXExact<TM> : kPiecesX<TM>>(X, at.x32, S, acc);
+    from_state<PL, C, D, kPiecesS<TIn, DG>>(X, at.x32, S, acc);
     scale_rows<C>(acc, dec[cur].out);
     if (more) fetch_v(t - C);
     if constexpr (DG)
-      if (is_dk) row_dots<TM, C, D>(acc, K, z0, part[wave - NW]);
+      if (is_dk) row_dots<PL, C, D>(acc, K, z0, part[wave - NW]);
     __syncthreads();
     if constexpr (DG)
       if (tid < C && t + tid < sp.n) {
@@ -271,7 +273,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
         rows[row0 + (int64_t)(t + tid) * pr.H] = s;
       }
     if (more) fetch_o(t - C);
-    within_chunk<TM, C, D, D, NP, kPiecesZ<TM>, true>(Y, Z, P[is_dk], dec[cur], at, S, acc);
+    within_chunk<PL, C, D, D, NP, true>(Y, Z, P[is_dk], dec[cur], at, S, acc);
     const int64_t ok = row0 * pr.Dk + (int64_t)t * kst, ov = row0 * pr.Dv + (int64_t)t * vst;
     if (is_dk) {
       if (shared) store_rows<float, C>(acc, a.dk_part + ok, kst, sp.n - t, pr.Dk, z0);
@@ -284,7 +286,7 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
     OutRegs<TIn, C, D, NT> outk, outv;
     if (!shared) outk.take((const TIn*)K);
     outv.take((const TIn*)V);
-    if constexpr (sizeof(TIn) != sizeof(TM)) __syncthreads();
+    if constexpr (PL != 1) __syncthreads();
     if (more) put_tiles();
     if (!shared) outk.put((TIn*)a.dk + ok, kst, sp.n - t, pr.Dk);
     outv.put((TIn*)a.dv + ov, vst, sp.n - t, pr.Dv);
@@ -371,22 +373,22 @@ __global__ __launch_bounds__(256) void k_gate_total(const double* total, int slo
   }
 }
 
-template <class TIn, class TM, int DX, int NW>
+template <class TIn, int DX, int NW>
 static hipError_t dq_dims(const BwdArgs& a, hipStream_t st) {
   const unsigned blocks = (unsigned)((int64_t)a.pr.slots * a.pr.H);
-  if (a.dg) hipLaunchKernelGGL((k_attn_dq<TIn, TM, DX, NW, true>), dim3(blocks), dim3(NW * 64), 0, st, a);
-  else hipLaunchKernelGGL((k_attn_dq<TIn, TM, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, a);
+  if (a.dg) hipLaunchKernelGGL((k_attn_dq<TIn, DX, NW, true>), dim3(blocks), dim3(NW * 64), 0, st, a);
+  else hipLaunchKernelGGL((k_attn_dq<TIn, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, a);
   return hipGetLastError();
 }
-template <class TIn, class TM, int D>
+template <class TIn, int D>
 static hipError_t dkv_dims(const BwdArgs& a, hipStream_t st) {
   const unsigned blocks = (unsigned)((int64_t)a.pr.slots * a.pr.H);
-  if (a.dg) hipLaunchKernelGGL((k_attn_dkv<TIn, TM, D, true>), dim3(blocks), dim3(D * 4), 0, st, a);
-  else hipLaunchKernelGGL((k_attn_dkv<TIn, TM, D, false>), dim3(blocks), dim3(D * 4), 0, st, a);
+  if (a.dg) hipLaunchKernelGGL((k_attn_dkv<TIn, D, true>), dim3(blocks), dim3(D * 4), 0, st, a);
+  else hipLaunchKernelGGL((k_attn_dkv<TIn, D, false>), dim3(blocks), dim3(D * 4), 0, st, a);
   return hipGetLastError();
 }
 
-template <class TIn, class TM>
+template <class TIn>
 static hipError_t bwd_type(const BwdArgs& a, int dtype, hipStream_t st) {
   const LaProblem& pr = a.pr;
   hipError_t e;
@@ -397,10 +399,10 @@ static hipError_t bwd_type(const BwdArgs& a, int dtype, hipStream_t st) {
     if ((e = launch_join(pr, true, a.dht, a.lams, a.totals, st)) != hipSuccess) return e;
   }
   const bool k64 = pr.Dk <= 64, v64 = pr.Dv <= 64;
-  e = v64 ? (k64 ? dq_dims<TIn, TM, 64, 2>(a, st) : dq_dims<TIn, TM, 64, 4>(a, st))
-          : (k64 ? dq_dims<TIn, TM, 128, 2>(a, st) : dq_dims<TIn, TM, 128, 4>(a, st));
+  e = v64 ? (k64 ? dq_dims<TIn, 64, 2>(a, st) : dq_dims<TIn, 64, 4>(a, st))
+          : (k64 ? dq_dims<TIn, 128, 2>(a, st) : dq_dims<TIn, 128, 4>(a, st));
   if (e != hipSuccess) return e;
-  e = k64 && v64 ? dkv_dims<TIn, TM, 64>(a, st) : dkv_dims<TIn, TM, 128>(a, st);
+  e = k64 && v64 ? dkv_dims<TIn, 64>(a, st) : dkv_dims<TIn, 128>(a, st);
   if (e != hipSuccess) return e;
   if (a.dq_part) {
     const int64_t n = pr.B * pr.T * pr.Hk * pr.Dk / 4, want = (n + 255) / 256;
@@ -424,9 +426,9 @@ static hipError_t bwd_type(const BwdArgs& a, int dtype, hipStream_t st) {
 }
 
 hipError_t launch_bwd(const BwdArgs& a, int dtype, hipStream_t st) {
-  if (dtype == 0) return bwd_type<float, float>(a, dtype, st);
-  if (dtype == 1) return bwd_type<__bf16, __bf16>(a, dtype, st);
-  return bwd_type<_Float16, float>(a, dtype, st);
+  if (dtype == 0) return bwd_type<float>(a, dtype, st);
+  if (dtype == 1) return bwd_type<__bf16>(a, dtype, st);
+  return bwd_type<_Float16>(a, dtype, st);
 }
 
 }  // namespace la

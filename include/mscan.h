@@ -245,9 +245,10 @@ MSCAN_API mscan_status matrix_affine_scan_bwd(const mscan_problem* prob, int k, 
  *  Types.     q, k, v, o and their gradients share one dtype (MSCAN_F32,
  *             MSCAN_BF16 or MSCAN_F16). Log decays, states and their gradients
  *             are fp32. Sums, decays and states are held in fp32 (log decays
- *             are added up in fp64); bf16 products run on the matrix cores with
- *             every fp32 operand split into bf16 pieces, so states and gate
- *             gradients keep fp32 precision. Results are bit-reproducible.
+ *             are added up in fp64). Products run on the bf16 matrix cores,
+ *             every operand of more than 8 bits as a sum of two or three bf16
+ *             pieces, so that states, gate gradients and fp32 results keep fp32
+ *             precision; magnitudes stay below 3.3e38, bf16's largest. Results are bit-reproducible.
  *  Layout.    q, k: [B][T][Hk][Dk], v: [B][T][H][Dv], strided
  *             (mscan_heads), last axis contiguous, 16-byte aligned pointers and
  *             strides of whole 16 bytes. H is a multiple of Hk; head h reads
@@ -282,7 +283,7 @@ typedef struct {
 
 /* Workspace bytes of linear_attention_fwd (backward = 0) or _bwd (1); pure host
  * function, 0 for an invalid problem. */
-MSCAN_API size_t linear_attention_workspace_bytes(const mscan_attention* prob, int backward);
+MSCAN_API size_t linear_attention_workspace_bytes(const mscan_attention* prob, int dtype, int backward);
 
 /* o and, if ht is not NULL, the state after each sequence. */
 MSCAN_API mscan_status linear_attention_fwd(const mscan_attention* prob, int dtype, const mscan_heads* q,

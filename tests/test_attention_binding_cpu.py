@@ -138,13 +138,13 @@ def problem(B=2, T=5, H=4, Hk=2, Dk=16, Dv=24, cu=0, nseg=2, scale=1.0, gs=(20, 
 
 def test_abi_sizes_its_workspaces(m):
     ws = m.lib.linear_attention_workspace_bytes
-    assert ws(problem(), 0) > 0 and ws(problem(), 1) > 0 and ws(problem(), 2) == 0
+    assert ws(problem(), 1, 0) > 0 and ws(problem(), 0, 1) > 0 and ws(problem(), 1, 2) == 0 and ws(problem(), 3, 0) == 0
     big = problem(B=1, T=65536, nseg=1, Dk=128, Dv=128)
-    assert ws(big, 0) > 65536 and ws(big, 1) > 2 * (ws(big, 0) - 256)
+    assert ws(big, 1, 0) > 65536 and ws(big, 1, 1) > ws(big, 1, 0)
     for bad in (problem(B=0), problem(T=0), problem(T=1 << 31), problem(H=3), problem(Hk=0), problem(Dk=12),
                 problem(Dk=136), problem(Dv=0), problem(nseg=1), problem(B=2, cu=P), problem(B=1, cu=P + 2, nseg=1),
                 problem(B=1, cu=P, nseg=0), problem(B=1 << 23, nseg=1 << 23)):
-        assert ws(bad, 0) == 0
+        assert ws(bad, 1, 0) == 0
     nb = m.lib.qk_norm_rope_workspace_bytes
     assert nb(norm()) > 0 and nb(norm(D=12)) == 0
 
@@ -169,7 +169,7 @@ def test_abi_refuses_attention(m):
     assert fwd(h0=P + 8) == INVALID and fwd(ht=P + 4) == INVALID
     assert fwd(prob=problem(B=1, T=1 << 30, H=64, Hk=1, nseg=1 << 20, cu=P)) == UNSUPPORTED
     big = problem(B=1, T=65536, nseg=1)
-    need = m.lib.linear_attention_workspace_bytes(big, 0)
+    need = m.lib.linear_attention_workspace_bytes(big, 1, 0)
     assert fwd(prob=big) == WORKSPACE and fwd(prob=big, ws=P + 8, n=need) == WORKSPACE
     assert fwd(prob=big, ws=P, n=need - 1024) == WORKSPACE
 
