@@ -56,6 +56,22 @@ __global__ __launch_bounds__(256) void k_attn_step(const StepArgs a) {
   const bool in = col < a.Dv;
   const int32_t slot = a.slots ? a.slots[b0] : b0;
   const bool live = slot >= 0 && slot < a.pool;
+  // a row's own inputs, one entry of q and k to a thread
+  float qv, kv, gv;
+  f4v v;
+  const auto fetch = [&](int b) {
+    const TIn* qp = (const TIn*)a.q.p + (int64_t)b * a.q.sb + (int64_t)(h / a.q.share) * a.q.sh;
+    const TIn* kp = (const TIn*)a.k.p + (int64_t)b * a.k.sb + (int64_t)(h / a.k.share) * a.k.sh;
+    const TIn* vp = (const TIn*)a.v.p + (int64_t)b * a.v.sb + (int64_t)h * a.v.sh;
+    qv = tid < a.Dk ? widen<TIn>(qp[tid]) * a.scale : 0.f;
+    kv = tid < a.Dk ? widen<TIn>(kp[tid]) : 0.f;
+    gv = a.g[(int64_t)b * a.gsb + (int64_t)h * a.gsh];
+    v = f4v{0.f, 0.f, 0.f, 0.f};
+    if (in)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) v[j] = widen<TIn>(vp[col + j]);
+  };
+  fetch(b0);
   float* sp = a.state + ((int64_t)(live ? slot : 0) * a.H + h) * a.Dk * a.Dv + col;
   f4v S[N];
 #pragma unroll
@@ -67,25 +83,17 @@ __global__ __launch_bounds__(256) void k_attn_step(const StepArgs a) {
   // the loads above are in flight; what is read of a state another row owns is dropped
   if (a.slots && live && slot_taken_before(a.slots, b0, slot)) return;
   for (int b = b0; b < a.B;) {
-    const TIn* qp = (const TIn*)a.q.p + (int64_t)b * a.q.sb + (int64_t)(h / a.q.share) * a.q.sh;
-    const TIn* kp = (const TIn*)a.k.p + (int64_t)b * a.k.sb + (int64_t)(h / a.k.share) * a.k.sh;
-    const TIn* vp = (const TIn*)a.v.p + (int64_t)b * a.v.sb + (int64_t)h * a.v.sh;
     TIn* op = (TIn*)a.o + ((int64_t)b * a.H + h) * a.Dv;
     if (!live) {  // no state: a zero output
       if (r0 == 0 && in)
         for (int j = 0; j < 4; ++j) op[col + j] = (TIn)0.f;
       return;
     }
-    for (int i = tid; i < DK; i += 256) {
-      qs[i] = i < a.Dk ? widen<TIn>(qp[i]) * a.scale : 0.f;
-      ks[i] = i < a.Dk ? widen<TIn>(kp[i]) : 0.f;
+    if (tid < DK) {
+      qs[tid] = qv;
+      ks[tid] = kv;
     }
-    const float g = a.g[(int64_t)b * a.gsb + (int64_t)h * a.gsh];
-    const float decay = exp2_fast((float)log2_decay(g));
-    f4v v = {0.f, 0.f, 0.f, 0.f};
-    if (in)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[j] = widen<TIn>(vp[col + j]);
+    const float decay = exp2_fast((float)log2_decay(gv));
     __syncthreads();
     f4v o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
@@ -107,6 +115,7 @@ __global__ __launch_bounds__(256) void k_attn_step(const StepArgs a) {
       for (int j = 0; j < 4; ++j) op[col + j] = (TIn)o[j];
     }
     b = a.slots ? next_with(a.slots, b, a.B, slot, &next) : a.B;
+    if (b < a.B) fetch(b);
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {

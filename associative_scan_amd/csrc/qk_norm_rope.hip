@@ -17,13 +17,16 @@ namespace mscan {
 namespace la {
 
 template <class T>
-__device__ __forceinline__ f4v load4(const T* p) {
-  typedef T t4 __attribute__((ext_vector_type(4)));
-  return __builtin_convertvector(__builtin_nontemporal_load((const t4*)p), f4v);
+struct Four {
+  typedef T type __attribute__((ext_vector_type(4)));
+};
+template <class T>
+__device__ __forceinline__ f4v wide(T v) {
+  return __builtin_convertvector(v, f4v);
 }
 template <class T>
 __device__ __forceinline__ void store4(T* p, f4v v) {
-  typedef T t4 __attribute__((ext_vector_type(4)));
+  typedef typename Four<T>::type t4;
   __builtin_nontemporal_store(__builtin_convertvector(v, t4), (t4*)p);
 }
 __device__ __forceinline__ f4v load_weight(const void* w, int dtype, int at) {
@@ -74,12 +77,12 @@ __device__ __forceinline__ Place place_of(const NormProblem& p, int lane) {
 struct Angles {
   f4v c, s;
 };
-__device__ __forceinline__ Angles load_angles(const NormProblem& p, int64_t b, int64_t t, int lane) {
-  int64_t pos = t;
-  if (p.positions) {
-    const int64_t at = p.per_batch ? b * p.T + t : t;
-    pos = p.positions64 ? ((const int64_t*)p.positions)[at] : (int64_t)((const int32_t*)p.positions)[at];
-  }
+__device__ __forceinline__ int64_t position_of(const NormProblem& p, int64_t b, int64_t t) {
+  if (!p.positions) return t;
+  const int64_t at = p.per_batch ? b * p.T + t : t;
+  return p.positions64 ? ((const int64_t*)p.positions)[at] : (int64_t)((const int32_t*)p.positions)[at];
+}
+__device__ __forceinline__ Angles load_angles(const NormProblem& p, int64_t pos, int lane) {
   pos = pos < 0 ? 0 : (pos >= p.table ? p.table - 1 : pos);
   const int64_t at = pos * (p.rot / 2) + lane * 4;
   return Angles{*(const f4v*)(p.cos + at), *(const f4v*)(p.sin + at)};
@@ -118,45 +121,79 @@ struct Rows {
   }
 };
 
+// A lane's part of HP heads, as it lies in memory.
+template <class TIn, int HP>
+struct Heads4 {
+  typedef typename Four<TIn>::type t4;
+  t4 u[HP], v[HP];
+  __device__ __forceinline__ void load(const Heads& x, int64_t b, int64_t t, int h0, int nh, const Place& at) {
+    const TIn* p = (const TIn*)x.p + b * x.sb + t * x.st + h0 * x.sh;
+#pragma unroll
+    for (int j = 0; j < HP; ++j) {
+      u[j] = t4{0, 0, 0, 0};
+      v[j] = t4{0, 0, 0, 0};
+      if (at.in && j < nh) {
+        u[j] = __builtin_nontemporal_load((const t4*)(p + j * x.sh + at.a));
+        v[j] = __builtin_nontemporal_load((const t4*)(p + j * x.sh + at.b));
+      }
+    }
+  }
+};
+
+// A workgroup goes over its share of the rows, the next rows and their angles on
+// their way while it works on the last ones: a position, its angles and the rows
+// are three trips to memory, of which a workgroup that ran one set of rows would
+// overlap none (80 us for 32767 tokens of 16 + 4 heads that way).
 template <class TIn, int L, int HP, bool PAIRS>
 __global__ __launch_bounds__(256) void k_norm_fwd(const NormProblem p, const NormSide q, const NormSide k,
                                                   unsigned qblocks) {
+  constexpr int G = 256 / L;
   const bool isq = blockIdx.x < qblocks;
   const NormSide& x = isq ? q : k;
-  const unsigned blk = isq ? blockIdx.x : blockIdx.x - qblocks;
+  const unsigned blk = isq ? blockIdx.x : blockIdx.x - qblocks, nblk = isq ? qblocks : gridDim.x - qblocks;
   const int lane = threadIdx.x % L;
-  const Rows<L, HP> r(p, x.heads, blk * (256 / L) + threadIdx.x / L);
   const Place at = place_of<PAIRS>(p, lane);
   const f4v zero = {0.f, 0.f, 0.f, 0.f}, one = {1.f, 1.f, 1.f, 1.f};
-  const TIn* xp = (const TIn*)x.x.p + r.b * x.x.sb + r.t * x.x.st + r.h0 * x.x.sh;
-  f4v u[HP], v[HP];
-#pragma unroll
-  for (int j = 0; j < HP; ++j) {
-    u[j] = zero;
-    v[j] = zero;
-    if (at.in && j < r.nh) {
-      u[j] = load4<TIn>(xp + j * x.x.sh + at.a);
-      v[j] = load4<TIn>(xp + j * x.x.sh + at.b);
-    }
-  }
-  Angles ang{one, zero};
-  f4v wu = zero, wv = zero;
-  if (at.in && r.nh) {
-    if (at.rotated) ang = load_angles(p, r.b, r.t, lane);
-    wu = load_weight(x.w, p.wtype, at.a);
-    wv = load_weight(x.w, p.wtype, at.b);
-  }
-  TIn* yp = (TIn*)x.y + ((r.b * p.T + r.t) * x.heads + r.h0) * p.D;
+  const uint32_t groups = (uint32_t)(p.B * p.T * ((x.heads + HP - 1) / HP));
+  const uint32_t first = blk * G + threadIdx.x / L, step = nblk * G;
+  const f4v wu = at.in ? load_weight(x.w, p.wtype, at.a) : zero, wv = at.in ? load_weight(x.w, p.wtype, at.b) : zero;
   const float inv = 1.f / (float)p.D;
-#pragma unroll
-  for (int j = 0; j < HP; ++j) {
-    const float rs = rsqrtf(row_sum<L>(dot4(u[j], u[j]) + dot4(v[j], v[j])) * inv + p.eps);
-    f4v a = u[j] * rs * wu, b = v[j] * rs * wv;
-    rotate<PAIRS>(a, b, ang, 1.f);
-    if (at.in && j < r.nh) {
-      store4<TIn>(yp + (int64_t)j * p.D + at.a, a);
-      store4<TIn>(yp + (int64_t)j * p.D + at.b, b);
+  const auto rows_of = [&](uint32_t g) { return Rows<L, HP>(p, x.heads, g < groups ? g : groups - 1); };
+  Rows<L, HP> r = rows_of(first);
+  Heads4<TIn, HP> in;
+  Angles ang{one, zero};
+  in.load(x.x, r.b, r.t, r.h0, r.nh, at);
+  int64_t pos = 0;
+  if (at.rotated) {
+    ang = load_angles(p, position_of(p, r.b, r.t), lane);
+    const Rows<L, HP> n = rows_of(first + step);
+    pos = position_of(p, n.b, n.t);
+  }
+  for (uint32_t g = first; g < groups; g += step) {
+    const Rows<L, HP> next = rows_of(g + step);
+    const Heads4<TIn, HP> now = in;
+    const Angles turn = ang;
+    if (g + step < groups) {
+      in.load(x.x, next.b, next.t, next.h0, next.nh, at);
+      if (at.rotated) {
+        ang = load_angles(p, pos, lane);
+        const Rows<L, HP> n = rows_of(g + 2 * step);
+        pos = position_of(p, n.b, n.t);
+      }
     }
+    TIn* yp = (TIn*)x.y + ((r.b * p.T + r.t) * x.heads + r.h0) * p.D;
+#pragma unroll
+    for (int j = 0; j < HP; ++j) {
+      const f4v u = wide(now.u[j]), v = wide(now.v[j]);
+      const float rs = rsqrtf(row_sum<L>(dot4(u, u) + dot4(v, v)) * inv + p.eps);
+      f4v a = u * rs * wu, b = v * rs * wv;
+      rotate<PAIRS>(a, b, turn, 1.f);
+      if (at.in && j < r.nh) {
+        store4<TIn>(yp + (int64_t)j * p.D + at.a, a);
+        store4<TIn>(yp + (int64_t)j * p.D + at.b, b);
+      }
+    }
+    r = next;
   }
 }
 
@@ -176,44 +213,53 @@ __global__ __launch_bounds__(256) void k_norm_bwd(const NormProblem p, const Nor
   const f4v zero = {0.f, 0.f, 0.f, 0.f}, one = {1.f, 1.f, 1.f, 1.f};
   const f4v wu = at.in ? load_weight(x.w, p.wtype, at.a) : zero, wv = at.in ? load_weight(x.w, p.wtype, at.b) : zero;
   const float inv = 1.f / (float)p.D;
-  const int64_t groups = p.B * p.T * ((x.heads + HP - 1) / HP);
+  const uint32_t groups = (uint32_t)(p.B * p.T * ((x.heads + HP - 1) / HP));
+  const uint32_t first = blk * G + threadIdx.x / L, step = nblk * G;
+  const auto rows_of = [&](uint32_t g) { return Rows<L, HP>(p, x.heads, g < groups ? g : groups - 1); };
+  Rows<L, HP> r = rows_of(first);
+  Heads4<TIn, HP> in, din;
+  Angles ang{one, zero};
+  in.load(x.x, r.b, r.t, r.h0, r.nh, at);
+  din.load(x.dy, r.b, r.t, r.h0, r.nh, at);
+  int64_t pos = 0;
+  if (at.rotated) {
+    ang = load_angles(p, position_of(p, r.b, r.t), lane);
+    const Rows<L, HP> n = rows_of(first + step);
+    pos = position_of(p, n.b, n.t);
+  }
   f4v du = zero, dv = zero;
-  for (int64_t g0 = (int64_t)blk * G; g0 < groups; g0 += (int64_t)nblk * G) {
-    const Rows<L, HP> r(p, x.heads, (uint32_t)g0 + threadIdx.x / L);
-    const TIn* xp = (const TIn*)x.x.p + r.b * x.x.sb + r.t * x.x.st + r.h0 * x.x.sh;
-    const TIn* dp = (const TIn*)x.dy.p + r.b * x.dy.sb + r.t * x.dy.st + r.h0 * x.dy.sh;
-    f4v u[HP], v[HP], a[HP], b[HP];
-#pragma unroll
-    for (int j = 0; j < HP; ++j) {
-      u[j] = zero;
-      v[j] = zero;
-      a[j] = zero;
-      b[j] = zero;
-      if (at.in && j < r.nh) {
-        u[j] = load4<TIn>(xp + j * x.x.sh + at.a);
-        v[j] = load4<TIn>(xp + j * x.x.sh + at.b);
-        a[j] = load4<TIn>(dp + j * x.dy.sh + at.a);
-        b[j] = load4<TIn>(dp + j * x.dy.sh + at.b);
+  for (uint32_t g = first; g < groups; g += step) {
+    const Rows<L, HP> next = rows_of(g + step);
+    const Heads4<TIn, HP> now = in, dnow = din;
+    const Angles turn = ang;
+    if (g + step < groups) {
+      in.load(x.x, next.b, next.t, next.h0, next.nh, at);
+      din.load(x.dy, next.b, next.t, next.h0, next.nh, at);
+      if (at.rotated) {
+        ang = load_angles(p, pos, lane);
+        const Rows<L, HP> n = rows_of(g + 2 * step);
+        pos = position_of(p, n.b, n.t);
       }
     }
-    Angles ang{one, zero};
-    if (at.rotated && r.nh) ang = load_angles(p, r.b, r.t, lane);
     TIn* yp = (TIn*)x.y + ((r.b * p.T + r.t) * x.heads + r.h0) * p.D;
 #pragma unroll
     for (int j = 0; j < HP; ++j) {
-      rotate<PAIRS>(a[j], b[j], ang, -1.f);
-      const float rs = rsqrtf(row_sum<L>(dot4(u[j], u[j]) + dot4(v[j], v[j])) * inv + p.eps);
-      const f4v hu = u[j] * rs, hv = v[j] * rs, tu = a[j] * wu, tv = b[j] * wv;
+      f4v a = wide(dnow.u[j]), b = wide(dnow.v[j]);
+      rotate<PAIRS>(a, b, turn, -1.f);
+      const f4v u = wide(now.u[j]), v = wide(now.v[j]);
+      const float rs = rsqrtf(row_sum<L>(dot4(u, u) + dot4(v, v)) * inv + p.eps);
+      const f4v hu = u * rs, hv = v * rs, tu = a * wu, tv = b * wv;
       const float m = row_sum<L>(dot4(tu, hu) + dot4(tv, hv)) * inv;
       if (j < r.nh) {
-        du += a[j] * hu;
-        dv += b[j] * hv;
+        du += a * hu;
+        dv += b * hv;
         if (at.in) {
           store4<TIn>(yp + (int64_t)j * p.D + at.a, (tu - hu * m) * rs);
           store4<TIn>(yp + (int64_t)j * p.D + at.b, (tv - hv * m) * rs);
         }
       }
     }
+    r = next;
   }
   if (at.in) {
 #pragma unroll
@@ -255,42 +301,40 @@ __global__ __launch_bounds__(256) void k_norm_weights(const float* partial, int 
 
 static int norm_lanes(int D) { return D <= 64 ? 8 : D <= 128 ? 16 : 32; }
 
-template <int HP>
-static int64_t norm_groups(const NormProblem& p, int heads) {
-  return p.B * p.T * ((heads + HP - 1) / HP);
-}
-
-template <class TIn, int L, bool PAIRS>
-static hipError_t fwd_lanes(const NormProblem& p, const NormSide& q, const NormSide& k, hipStream_t st) {
-  // several heads per lane group once there is a wave for every SIMD of the card
-  constexpr int HP = 4;
-  if (p.B * p.T * (q.heads + k.heads) * L >= (int64_t)1024 * 64 * HP) {
-    const unsigned qb = (unsigned)((norm_groups<HP>(p, q.heads) * L + 255) / 256);
-    const unsigned kb = (unsigned)((norm_groups<HP>(p, k.heads) * L + 255) / 256);
-    hipLaunchKernelGGL((k_norm_fwd<TIn, L, HP, PAIRS>), dim3(qb + kb), dim3(256), 0, st, p, q, k, qb);
-  } else {
-    const unsigned qb = (unsigned)((norm_groups<1>(p, q.heads) * L + 255) / 256);
-    const unsigned kb = (unsigned)((norm_groups<1>(p, k.heads) * L + 255) / 256);
-    hipLaunchKernelGGL((k_norm_fwd<TIn, L, 1, PAIRS>), dim3(qb + kb), dim3(256), 0, st, p, q, k, qb);
-  }
-  return hipGetLastError();
-}
-
-// Workgroups of the backward pass, q's and k's: enough to fill the card, few
-// enough that the partial sums of dw stay small.
-void norm_bwd_blocks(const NormProblem& p, int Hq, int Hk, unsigned& qb, unsigned& kb) {
+// Workgroups for q's and k's rows: all that there are, or `most` shared out by
+// their number.
+static void norm_blocks(const NormProblem& p, int Hq, int Hk, int hp, int64_t most, unsigned& qb, unsigned& kb) {
   const int L = norm_lanes(p.D);
-  const int64_t nq = (norm_groups<2>(p, Hq) * L + 255) / 256, nk = (norm_groups<2>(p, Hk) * L + 255) / 256;
-  const int64_t most = 2048;
+  const int64_t nq = (p.B * p.T * ((Hq + hp - 1) / hp) * L + 255) / 256;
+  const int64_t nk = (p.B * p.T * ((Hk + hp - 1) / hp) * L + 255) / 256;
   if (nq + nk <= most) {
     qb = (unsigned)nq;
     kb = (unsigned)nk;
     return;
   }
-  qb = (unsigned)(most * nq / (nq + nk));
-  if (qb < 1) qb = 1;
-  if (qb > most - 1) qb = (unsigned)(most - 1);
+  const int64_t n = most * nq / (nq + nk);
+  qb = (unsigned)(n < 1 ? 1 : n > most - 1 ? most - 1 : n);
   kb = (unsigned)(most - qb);
+}
+constexpr int kBwdHeads = 2;
+// The backward's partial sums of dw are one row per workgroup: few enough to stay
+// small, enough to fill the card.
+void norm_bwd_blocks(const NormProblem& p, int Hq, int Hk, unsigned& qb, unsigned& kb) {
+  norm_blocks(p, Hq, Hk, kBwdHeads, 2048, qb, kb);
+}
+
+template <class TIn, int L, int HP, bool PAIRS>
+static hipError_t fwd_heads(const NormProblem& p, const NormSide& q, const NormSide& k, hipStream_t st) {
+  unsigned qb, kb;
+  norm_blocks(p, q.heads, k.heads, HP, 2048, qb, kb);
+  hipLaunchKernelGGL((k_norm_fwd<TIn, L, HP, PAIRS>), dim3(qb + kb), dim3(256), 0, st, p, q, k, qb);
+  return hipGetLastError();
+}
+template <class TIn, int L, bool PAIRS>
+static hipError_t fwd_lanes(const NormProblem& p, const NormSide& q, const NormSide& k, hipStream_t st) {
+  // two heads per lane group once there is a wave for every SIMD of the card
+  return p.B * p.T * (q.heads + k.heads) * L >= (int64_t)1024 * 64 * 2 ? fwd_heads<TIn, L, 2, PAIRS>(p, q, k, st)
+                                                                       : fwd_heads<TIn, L, 1, PAIRS>(p, q, k, st);
 }
 
 template <class TIn, int L, bool PAIRS>
@@ -298,7 +342,7 @@ static hipError_t bwd_lanes(const NormProblem& p, const NormSide& q, const NormS
                             float* partial, hipStream_t st) {
   unsigned qb, kb;
   norm_bwd_blocks(p, q.heads, k.heads, qb, kb);
-  hipLaunchKernelGGL((k_norm_bwd<TIn, L, 2, PAIRS>), dim3(qb + kb), dim3(256), 0, st, p, q, k, qb, partial);
+  hipLaunchKernelGGL((k_norm_bwd<TIn, L, kBwdHeads, PAIRS>), dim3(qb + kb), dim3(256), 0, st, p, q, k, qb, partial);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || (!dwq && !dwk)) return e;
   hipLaunchKernelGGL(k_norm_weights, dim3(2 * p.D / 8), dim3(256), 0, st, partial, p.D, qb, kb, dwq, dwk);
