@@ -16,6 +16,7 @@ v [B, H, Dv], g [B, H] or [H], against state, fp32 [pool, H, Dk, Dv].
 from __future__ import annotations
 
 import contextlib
+import functools
 import struct
 
 import torch
@@ -120,13 +121,19 @@ def _states(t, shape, name, dev):
     return t
 
 
-def _space(prob, dtype, backward, dev):
+@functools.lru_cache(maxsize=4096)
+def _space_bytes(B, T, H, Hk, Dk, Dv, n, packed, dtype, backward):
+    prob = _ATTENTION.pack(B, T, H, Hk, Dk, Dv, 16 if packed else 0, n, 1.0, 0, 0, 0)  # the offsets are not read
+    return lib.linear_attention_workspace_bytes(prob, dtype, backward)
+
+
+def _space(q, shape, cu, dtype, backward):
     """A workspace of the call's own: torch's allocator keeps it in the stream's
     order, and in a captured graph's own pool."""
-    need = lib.linear_attention_workspace_bytes(prob, dtype, backward)
+    need = _space_bytes(*q.shape[:2], shape[1], q.shape[2], shape[2], shape[3], shape[0], cu is not None, dtype, backward)
     if need <= 256:
         return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=dev), need
+    return torch.empty(need, dtype=torch.uint8, device=q.device), need
 
 
 def linear_attention_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=None, need_ht=True):
@@ -143,7 +150,7 @@ def linear_attention_fwd(q, k, v, g, h0=None, cu_seqlens=None, scale=None, need_
             ht.zero_() if h0 is None else ht.copy_(h0)
         return o, ht
     with _on(dev):
-        ws, n = _space(prob, dt, 0, dev)
+        ws, n = _space(q, shape, cu, dt, 0)
         _check("linear_attention_fwd", lib.linear_attention_fwd(
             prob, dt, qh, kh, vh, g.data_ptr(), _ptr(h0), o.data_ptr(), _ptr(ht), _ptr(ws), n, _stream_handle(dev)))
     return o, ht
@@ -169,7 +176,7 @@ def linear_attention_bwd(q, k, v, g, do, h0=None, dht=None, cu_seqlens=None, sca
             dh0.zero_() if dht is None else dh0.copy_(dht)
         return dq, dk, dv, dg, dh0
     with _on(dev):
-        ws, n = _space(prob, dt, 1, dev)
+        ws, n = _space(q, shape, cu, dt, 1)
         _check("linear_attention_bwd", lib.linear_attention_bwd(
             prob, dt, qh, kh, vh, g.data_ptr(), oh, _ptr(h0), _ptr(dht), _ptr(dq), _ptr(dk), _ptr(dv), _ptr(dg),
             int(g.dim() == 1), _ptr(dh0), _ptr(ws), n, _stream_handle(dev)))

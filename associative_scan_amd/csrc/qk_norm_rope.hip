@@ -143,7 +143,7 @@ struct Heads4 {
 // A workgroup goes over its share of the rows, the next rows and their angles on
 // their way while it works on the last ones: a position, its angles and the rows
 // are three trips to memory, of which a workgroup that ran one set of rows would
-// overlap none (80 us for 32767 tokens of 16 + 4 heads that way).
+// overlap none.
 template <class TIn, int L, int HP, bool PAIRS>
 __global__ __launch_bounds__(256) void k_norm_fwd(const NormProblem p, const NormSide q, const NormSide k,
                                                   unsigned qblocks) {
@@ -326,14 +326,15 @@ void norm_bwd_blocks(const NormProblem& p, int Hq, int Hk, unsigned& qb, unsigne
 template <class TIn, int L, int HP, bool PAIRS>
 static hipError_t fwd_heads(const NormProblem& p, const NormSide& q, const NormSide& k, hipStream_t st) {
   unsigned qb, kb;
-  norm_blocks(p, q.heads, k.heads, HP, 2048, qb, kb);
+  norm_blocks(p, q.heads, k.heads, HP, 4096, qb, kb);
   hipLaunchKernelGGL((k_norm_fwd<TIn, L, HP, PAIRS>), dim3(qb + kb), dim3(256), 0, st, p, q, k, qb);
   return hipGetLastError();
 }
 template <class TIn, int L, bool PAIRS>
 static hipError_t fwd_lanes(const NormProblem& p, const NormSide& q, const NormSide& k, hipStream_t st) {
-  // two heads per lane group once there is a wave for every SIMD of the card
-  return p.B * p.T * (q.heads + k.heads) * L >= (int64_t)1024 * 64 * 2 ? fwd_heads<TIn, L, 2, PAIRS>(p, q, k, st)
+  // four heads per lane group once there is a wave for every SIMD of the card
+  // (32767 tokens of 16 + 4 heads: 77 us, with two 82 us, with one 95 us)
+  return p.B * p.T * (q.heads + k.heads) * L >= (int64_t)1024 * 64 * 4 ? fwd_heads<TIn, L, 4, PAIRS>(p, q, k, st)
                                                                        : fwd_heads<TIn, L, 1, PAIRS>(p, q, k, st);
 }
 
