@@ -240,11 +240,11 @@ __device__ __forceinline__ void weigh(const bf8 (&z)[PL], const float* f, int js
   split8<NS>(w, piece);
 }
 // S = e^{b_C} S + Y^T (in Z) and, with P, acc += P Z on the same reads of Z.
-template <int PL, int C, int DX, int DZ, int NP, bool REV>
+template <int PL, int C, int DX, int DZ, int NP, bool REV, int NS = kPiecesZ>
 __device__ __forceinline__ void within_chunk(const bf16* Y, const bf16* Z, const bf16* P, const Decays<C>& d,
                                              const LaneOffsets<C, DX, DZ>& at, f16v (&S)[DX / 32],
                                              f16v (&acc)[C / 32]) {
-  constexpr int RT = C / 32, KP = NP > 0 ? NP : 1, JS = C / 16, NS = kPiecesZ;
+  constexpr int RT = C / 32, KP = NP > 0 ? NP : 1, JS = C / 16;
   bf8 z[2][PL], y[DX / 32], pf[RT][KP], piece[2][NS];
   const int oy = fresh(at.y), oz = fresh(at.z), op = fresh(at.p);
   const auto inside = [](int rt, int js) { return REV ? js * 16 >= rt * 32 : js * 16 < rt * 32 + 32; };
@@ -354,6 +354,21 @@ __device__ __forceinline__ void load_state_t(f16v (&S)[DX / 32], const float* p,
     }
 }
 
+template <int DX>
+__device__ __forceinline__ void store_state_t(const f16v (&S)[DX / 32], float* p, int ldz, int dx, int dz, int z0) {
+  const int l = fresh_lane(), z = z0 + (l & 31), r0 = (l >> 5) << 3;
+  const int n = z < dz ? dx - r0 : 0;
+  p += r0 + (int64_t)z * ldz;
+#pragma unroll
+  for (int t = 0; t < DX / 32; ++t)
+#pragma unroll
+    for (int a = 0; a < 4; ++a) {
+      const int x = t * 32 + (a >> 1) * 16 + (a & 1) * 4;
+      const f4v v = {S[t][a * 4], S[t][a * 4 + 1], S[t][a * 4 + 2], S[t][a * 4 + 3]};
+      if (x < n) *(f4v*)(p + x) = v;
+    }
+}
+
 template <int CTRL>
 __device__ __forceinline__ float ror_add(float x) {
   return x + __builtin_bit_cast(float, __builtin_amdgcn_update_dpp(0, __builtin_bit_cast(int, x), CTRL, 0xf, 0xf, false));
@@ -440,7 +455,7 @@ struct OutRegs {
   static constexpr int STEP = NT / (D / 8), N = C / STEP, W = sizeof(TOut) == 4 ? 2 : 1;
   u4v r[N][W];
   __device__ __forceinline__ void take(const TOut* tile) {
-    const unsigned tid = fresh_thread();
+    const unsigned tid = fresh_thread<NT>();
     const int off = unit_at<TOut, D>((int)(tid / (D / 8)), (int)(tid % (D / 8)) * (8 / kUnit<TOut>));
 #pragma unroll
     for (int i = 0; i < N; ++i)
@@ -449,7 +464,7 @@ struct OutRegs {
   }
   __device__ __forceinline__ void put(TOut* out, int64_t st, int n, int d) const {
     const Window w = window<TOut, C>(out, st, d, n);
-    const unsigned tid = fresh_thread(), row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
+    const unsigned tid = fresh_thread<NT>(), row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
     const uint32_t step = STEP * (uint32_t)st * sizeof(TOut);
     uint32_t off = (int)c < d ? (row0 * (uint32_t)st + c) * sizeof(TOut) : kOutside;
 #pragma unroll

@@ -47,8 +47,10 @@ __device__ __forceinline__ int fresh(int x) {
   asm volatile("" : "+v"(x));
   return x;
 }
+// A thread's place among NT (a power of two): a workgroup's, or those of one role in it.
+template <int NT>
 __device__ __forceinline__ unsigned fresh_thread() {
-  unsigned t = threadIdx.x;
+  unsigned t = threadIdx.x & (NT - 1);
   asm volatile("" : "+v"(t));
   return t;
 }
@@ -243,7 +245,7 @@ struct TileRegs {
 
   __device__ __forceinline__ void load(const TIn* base, int64_t st, int d, int nrows) {
     const Window w = window<TIn, C>(base, st, d, nrows);
-    const unsigned tid = fresh_thread(), row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
+    const unsigned tid = fresh_thread<NT>(), row0 = tid / (D / 8), c = (tid % (D / 8)) * 8;
     const uint32_t step = STEP * (uint32_t)st * sizeof(TIn);
     uint32_t off = (row0 * (uint32_t)st + c) * sizeof(TIn);
     const int n = (int)c < d ? nrows - (int)row0 : 0;
@@ -258,7 +260,7 @@ struct TileRegs {
   // as kPlanes<TIn> tiles of C x D, one behind the other
   __device__ __forceinline__ void store(bf16* tile) const {
     constexpr int PL = kPlanes<TIn>;
-    const unsigned tid = fresh_thread();
+    const unsigned tid = fresh_thread<NT>();
     const int off = unit_at<bf16, D>((int)(tid / (D / 8)), (int)(tid % (D / 8)));
 #pragma unroll
     for (int i = 0; i < N; ++i) {

@@ -136,95 +136,87 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   }
 }
 
-// dk and dv. D: columns of every tile; NW waves for dv, then NW for dk.
-template <class TIn, int D, bool DG>
-__global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
-  constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, NW = D / 32, NT = NW * 128, NP = kPiecesP<TIn>;
-  __shared__ __align__(16) bf16 Q[PL * C * D];
-  __shared__ __align__(16) bf16 K[PL * C * D];  // and then the chunk's dk
-  __shared__ __align__(16) bf16 V[PL * C * D];  // and then the chunk's dv
-  __shared__ __align__(16) bf16 O[PL * C * D];
-  __shared__ __align__(16) bf16 P[2][NP * C * C];
-  __shared__ __align__(16) Decays<C> dec[2];
-  __shared__ float part[NW][C];
-  __shared__ float sums[kTiles<C>][2][16];
+// dk and dv. DK, DV: columns of k, q and of v, do; DV / 32 waves for dv, then
+// DK / 32 for dk, each with two of the four tiles to load. Lam is held twice, once
+// each way round. The dk waves' has three pieces (it gives the gates' gradients
+// and dh0), dv only needs two.
+template <class TIn, int DK, int DV>
+struct DkvTiles {
+  static constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>;
+  bf16 Q[PL * C * DK];
+  bf16 K[PL * C * DK];  // and then the chunk's dk
+  bf16 V[PL * C * DV];  // and then the chunk's dv
+  bf16 O[PL * C * DV];
+  bf16 P[2][kPiecesP<TIn> * C * C];
+  Decays<C> dec[2];
+  float part[DK / 32][C];
+  float sums[kTiles<C>][2][16];
+};
+template <class TIn, int DK, int DV, bool DG, bool IS_DK>
+__device__ __forceinline__ void dkv_span(const BwdArgs& a, const Span& sp, int slot, int h,
+                                         DkvTiles<TIn, DK, DV>& sh) {
+  constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, NK = DK / 32, NV = DV / 32, NW = NK + NV, NT = (IS_DK ? NK : NV) * 64,
+                NP = kPiecesP<TIn>, DX = IS_DK ? DV : DK, DZ = IS_DK ? DK : DV, NS = IS_DK ? kPiecesS<TIn, DG> : kPiecesS<TIn, false>,
+                NZ = IS_DK ? kPiecesZ : kPiecesS<TIn, false>;
+  constexpr bool GATE = IS_DK && DG;
   const LaProblem& pr = a.pr;
-  const int tid = threadIdx.x, wave = wave_id();
-  const bool is_dk = wave >= NW;
-  const int z0 = (is_dk ? wave - NW : wave) * 32;
-  const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
-  const Span sp = find_span(pr, slot);
+  const int tid = threadIdx.x, wave = wave_id(), z0 = (IS_DK ? wave - NV : wave) * 32;
   const int64_t row0 = (sp.batch * pr.T + sp.t0) * pr.H + h;
-  const bool shared = a.dk_part != nullptr;
-  const int64_t kst = (int64_t)pr.H * pr.Dk, vst = (int64_t)pr.H * pr.Dv;
+  const bool shared = IS_DK && a.dk_part != nullptr;
   float* rows = a.rows + pr.B * pr.T * pr.H;
-  if (pr.cu && sp.seq >= pr.nseg) {
-    for (int64_t i = tid; i < (int64_t)sp.n * pr.Dk; i += NT) {
-      const int64_t at = row0 * pr.Dk + i / pr.Dk * kst + i % pr.Dk;
-      if (shared) a.dk_part[at] = 0.f;
-      else ((TIn*)a.dk)[at] = (TIn)0.f;
-    }
-    for (int64_t i = tid; i < (int64_t)sp.n * pr.Dv; i += NT)
-      ((TIn*)a.dv)[row0 * pr.Dv + i / pr.Dv * vst + i % pr.Dv] = (TIn)0.f;
-    return;
-  }
-  if (sp.n == 0 && !sp.is_first) return;
   const int64_t cells = (int64_t)pr.Dk * pr.Dv, state = ((int64_t)slot * pr.H + h) * cells;
   const int64_t outer = ((int64_t)sp.seq * pr.H + h) * cells;
   const float* lam = sp.is_last ? (a.dht ? a.dht + outer : nullptr) : a.lams + state;
-  f16v S[NW];
-  if (is_dk) load_state_t<D>(S, lam, pr.Dv, pr.Dv, pr.Dk, z0);
-  else load_state<D>(S, lam, pr.Dv, 1, pr.Dk, pr.Dv, z0);
-  const bf16* X = is_dk ? V : K;
-  const bf16* Y = is_dk ? O : Q;
-  const bf16* Z = is_dk ? Q : O;
-  const TIn* qp = head_base<TIn>(a.q, sp.batch, sp.t0, h);
-  const TIn* kp = head_base<TIn>(a.k, sp.batch, sp.t0, h);
-  const TIn* vp = head_base<TIn>(a.v, sp.batch, sp.t0, h);
-  const TIn* op = head_base<TIn>(a.dO, sp.batch, sp.t0, h);
+  f16v S[DX / 32];
+  if constexpr (IS_DK) load_state_t<DX>(S, lam, pr.Dv, pr.Dv, pr.Dk, z0);
+  else load_state<DX>(S, lam, pr.Dv, 1, pr.Dk, pr.Dv, z0);
+  const bf16* X = IS_DK ? sh.V : sh.K;
+  const bf16* Y = IS_DK ? sh.O : sh.Q;
+  const bf16* Z = IS_DK ? sh.Q : sh.O;
+  const Heads& h1 = IS_DK ? a.k : a.v;  // the role's own tiles
+  const Heads& h2 = IS_DK ? a.q : a.dO;
+  bf16* const T1 = IS_DK ? sh.K : sh.V;  // and then the chunk's output
+  bf16* const T2 = IS_DK ? sh.Q : sh.O;
+  const int dz = IS_DK ? pr.Dk : pr.Dv;
+  const TIn* p1 = head_base<TIn>(h1, sp.batch, sp.t0, h);
+  const TIn* p2 = head_base<TIn>(h2, sp.batch, sp.t0, h);
   const float* gp = gate_base(pr, sp.batch, sp.t0, h);
-  TileRegs<TIn, C, D, NT> rq, rk, rv, ro;
+  TileRegs<TIn, C, DZ, NT> r1, r2;
   float rg = 0.f;
-  const auto fetch_k = [&](int t) {
-    rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t);
-    if (wave == 2 * NW - 1) rg = load_gate(gp, pr.gst, t, sp.n);
+  const bool decays = !IS_DK && wave == 0;  // this wave's work besides
+  const auto fetch1 = [&](int t) {
+    r1.load(p1 + (int64_t)t * h1.st, h1.st, dz, sp.n - t);
+    if (decays) rg = load_gate(gp, pr.gst, t, sp.n);
   };
-  const auto fetch_q = [&](int t) { rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t); };
-  const auto fetch_v = [&](int t) { rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t); };
-  const auto fetch_o = [&](int t) { ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t); };
-  const auto put_tiles = [&] {
-    rq.store(Q);
-    rk.store(K);
-    rv.store(V);
-    ro.store(O);
-  };
-  const LaneOffsets<C, D, D> at(z0);
+  const auto fetch2 = [&](int t) { r2.load(p2 + (int64_t)t * h2.st, h2.st, dz, sp.n - t); };
+  const LaneOffsets<C, DX, DZ> at(z0);
+  const int k16 = row_lane<DK, 16>(), v16 = row_lane<DV, 16>();
   const int last = sp.n > 0 ? (sp.n - 1) / C * C : -C;
   if (last >= 0) {
-    fetch_k(last);
-    fetch_q(last);
-    fetch_v(last);
-    fetch_o(last);
-    put_tiles();
-    if (wave == 2 * NW - 1) write_decays<C, true>(dec[0], rg, pr.scale);
+    fetch1(last);
+    fetch2(last);
+    r1.store(T1);
+    r2.store(T2);
+    if (decays) write_decays<C, true>(sh.dec[0], rg, pr.scale);
   }
   settle();
   __syncthreads();
   for (int t = last, cur = 0; t >= 0; t -= C, cur ^= 1) {
     const bool more = t > 0;
-    if (more) fetch_k(t - C);
+    if (more) fetch1(t - C);
     {  // scores of both roles, and W's sums over i and over j
       const int l = fresh_lane();
-      for (int i = wave; i < kTiles<C>; i += 2 * NW) {
+      for (int i = wave; i < kTiles<C>; i += NW) {
         int rt, ct;
         tile_of<C, true>(i, rt, ct);
-        const f4v d = decay_tile<C, true>(dec[cur], rt, ct, l);
-        ScoreFrags<PL, C, D> fx, fy;
-        fx.read(K, Q, at.x16, rt, ct);
-        if (PL == 1) fy.read(V, O, at.x16, rt, ct);
+        const f4v d = decay_tile<C, true>(sh.dec[cur], rt, ct, l);
+        ScoreFrags<PL, C, DK> fx;
+        ScoreFrags<PL, C, DV> fy;
+        fx.read(sh.K, sh.Q, k16, rt, ct);
+        if (PL == 1) fy.read(sh.V, sh.O, v16, rt, ct);
         step_fence();
         f4v x = fx.product();
-        if (PL > 1) fy.read(V, O, at.x16, rt, ct);
+        if (PL > 1) fy.read(sh.V, sh.O, v16, rt, ct);
         f4v y = fy.product();
         float row[4], col = 0.f;
 #pragma unroll
@@ -236,63 +228,81 @@ __global__ __launch_bounds__(D * 4, 2) void k_attn_dkv(const BwdArgs a) {
           col += row[e];
           y[e] = d[e] != 0.f ? y[e] * f : 0.f;
         }
-        put_tile<C, NP>(P[0], x, rt, ct, l);
-        put_tile<C, NP>(P[1], y, rt, ct, l);
+        put_tile<C, NP>(sh.P[0], x, rt, ct, l);
+        put_tile<C, NP>(sh.P[1], y, rt, ct, l);
         if constexpr (DG) {
           col += __shfl_xor(col, 16);
           col += __shfl_xor(col, 32);
-          if (l < 16) sums[i][0][l] = col;
+          if (l < 16) sh.sums[i][0][l] = col;
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             row[e] = sum16(row[e]);
-            if ((l & 15) == e) sums[i][1][((l >> 4) << 2) + e] = row[e];
+            if ((l & 15) == e) sh.sums[i][1][((l >> 4) << 2) + e] = row[e];
           }
         }
       }
     }
-    if (more) fetch_q(t - C);
+    if (more) fetch2(t - C);
     f16v acc[C / 32];
-    from_state<PL, C, D, kPiecesS<TIn, DG>>(X, at.x32, S, acc);
-    scale_rows<C>(acc, dec[cur].out);
-    if (more) fetch_v(t - C);
-    if constexpr (DG)
-      if (is_dk) row_dots<PL, C, D>(acc, K, z0, part[wave - NW]);
+    from_state<PL, C, DX, NS>(X, at.x32, S, acc);
+    scale_rows<C>(acc, sh.dec[cur].out);
+    if constexpr (GATE) row_dots<PL, C, DK>(acc, sh.K, z0, sh.part[wave - NV]);
     __syncthreads();
-    if constexpr (DG)
+    if constexpr (DG && !IS_DK)
       if (tid < C && t + tid < sp.n) {
         float s = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) s -= part[w][tid];
+        for (int w = 0; w < NK; ++w) s -= sh.part[w][tid];
 #pragma unroll
         for (int i = 0; i < kTiles<C>; ++i) {
           int rt, ct;
           tile_of<C, true>(i, rt, ct);
-          if (ct == tid >> 4) s += sums[i][1][tid & 15];
-          if (rt == tid >> 4) s -= sums[i][0][tid & 15];
+          if (ct == tid >> 4) s += sh.sums[i][1][tid & 15];
+          if (rt == tid >> 4) s -= sh.sums[i][0][tid & 15];
         }
         rows[row0 + (int64_t)(t + tid) * pr.H] = s;
       }
-    if (more) fetch_o(t - C);
-    within_chunk<PL, C, D, D, NP, true>(Y, Z, P[is_dk], dec[cur], at, S, acc);
-    const int64_t ok = row0 * pr.Dk + (int64_t)t * kst, ov = row0 * pr.Dv + (int64_t)t * vst;
-    if (is_dk) {
-      if (shared) store_rows<float, C>(acc, a.dk_part + ok, kst, sp.n - t, pr.Dk, z0);
-      else rows_to_lds<TIn, C, D>(acc, (TIn*)K, z0);
-    } else {
-      rows_to_lds<TIn, C, D>(acc, (TIn*)V, z0);
-    }
-    if (more && wave == 2 * NW - 1) write_decays<C, true>(dec[cur ^ 1], rg, pr.scale);
+    within_chunk<PL, C, DX, DZ, NP, true, NZ>(Y, Z, sh.P[IS_DK], sh.dec[cur], at, S, acc);
+    const int64_t ost = (int64_t)pr.H * dz, o = row0 * dz + (int64_t)t * ost;
+    if (shared) store_rows<float, C>(acc, a.dk_part + o, ost, sp.n - t, dz, z0);
+    else rows_to_lds<TIn, C, DZ>(acc, (TIn*)T1, z0);
+    if (more && decays) write_decays<C, true>(sh.dec[cur ^ 1], rg, pr.scale);
     __syncthreads();
-    OutRegs<TIn, C, D, NT> outk, outv;
-    if (!shared) outk.take((const TIn*)K);
-    outv.take((const TIn*)V);
+    OutRegs<TIn, C, DZ, NT> out;
+    if (!shared) out.take((const TIn*)T1);
     if constexpr (PL != 1) __syncthreads();
-    if (more) put_tiles();
-    if (!shared) outk.put((TIn*)a.dk + ok, kst, sp.n - t, pr.Dk);
-    outv.put((TIn*)a.dv + ov, vst, sp.n - t, pr.Dv);
+    if (more) {
+      r1.store(T1);
+      r2.store(T2);
+    }
+    if (!shared) out.put((TIn*)(IS_DK ? a.dk : a.dv) + o, ost, sp.n - t, dz);
     __syncthreads();
   }
-  if (sp.is_first && a.dh0 && !is_dk) store_state<D>(S, a.dh0 + outer, pr.Dv, 1, pr.Dk, pr.Dv, z0);
+  if constexpr (IS_DK)
+    if (sp.is_first && a.dh0) store_state_t<DX>(S, a.dh0 + outer, pr.Dv, pr.Dv, pr.Dk, z0);
+}
+template <class TIn, int DK, int DV, bool DG>
+__global__ __launch_bounds__((DK + DV) * 2, 2) void k_attn_dkv(const BwdArgs a) {
+  constexpr int NT = (DK + DV) * 2;
+  __shared__ __align__(16) DkvTiles<TIn, DK, DV> sh;
+  const LaProblem& pr = a.pr;
+  const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
+  const Span sp = find_span(pr, slot);
+  if (pr.cu && sp.seq >= pr.nseg) {
+    const int64_t row0 = (sp.batch * pr.T + sp.t0) * pr.H + h;
+    for (int64_t i = threadIdx.x; i < (int64_t)sp.n * pr.Dk; i += NT) {
+      const int64_t at = row0 * pr.Dk + i / pr.Dk * pr.H * pr.Dk + i % pr.Dk;
+      if (a.dk_part) a.dk_part[at] = 0.f;
+      else ((TIn*)a.dk)[at] = (TIn)0.f;
+    }
+    for (int64_t i = threadIdx.x; i < (int64_t)sp.n * pr.Dv; i += NT)
+      ((TIn*)a.dv)[row0 * pr.Dv + i / pr.Dv * pr.H * pr.Dv + i % pr.Dv] = (TIn)0.f;
+    return;
+  }
+  if (sp.n == 0 && !sp.is_first) return;
+  // the roles meet at the same barriers, on the same path through the span
+  if (wave_id() < DV / 32) dkv_span<TIn, DK, DV, DG, false>(a, sp, slot, h, sh);
+  else dkv_span<TIn, DK, DV, DG, true>(a, sp, slot, h, sh);
 }
 
 // Gradients of shared heads: the sum over the heads that read one, in order.
@@ -380,11 +390,11 @@ static hipError_t dq_dims(const BwdArgs& a, hipStream_t st) {
   else hipLaunchKernelGGL((k_attn_dq<TIn, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, a);
   return hipGetLastError();
 }
-template <class TIn, int D>
+template <class TIn, int DK, int DV>
 static hipError_t dkv_dims(const BwdArgs& a, hipStream_t st) {
-  const unsigned blocks = (unsigned)((int64_t)a.pr.slots * a.pr.H);
-  if (a.dg) hipLaunchKernelGGL((k_attn_dkv<TIn, D, true>), dim3(blocks), dim3(D * 4), 0, st, a);
-  else hipLaunchKernelGGL((k_attn_dkv<TIn, D, false>), dim3(blocks), dim3(D * 4), 0, st, a);
+  const unsigned blocks = (unsigned)((int64_t)a.pr.slots * a.pr.H), threads = (DK + DV) * 2;
+  if (a.dg) hipLaunchKernelGGL((k_attn_dkv<TIn, DK, DV, true>), dim3(blocks), dim3(threads), 0, st, a);
+  else hipLaunchKernelGGL((k_attn_dkv<TIn, DK, DV, false>), dim3(blocks), dim3(threads), 0, st, a);
   return hipGetLastError();
 }
 
@@ -402,7 +412,8 @@ static hipError_t bwd_type(const BwdArgs& a, int dtype, hipStream_t st) {
   e = v64 ? (k64 ? dq_dims<TIn, 64, 2>(a, st) : dq_dims<TIn, 64, 4>(a, st))
           : (k64 ? dq_dims<TIn, 128, 2>(a, st) : dq_dims<TIn, 128, 4>(a, st));
   if (e != hipSuccess) return e;
-  e = k64 && v64 ? dkv_dims<TIn, 64>(a, st) : dkv_dims<TIn, 128>(a, st);
+  e = v64 ? (k64 ? dkv_dims<TIn, 64, 64>(a, st) : dkv_dims<TIn, 128, 64>(a, st))
+          : (k64 ? dkv_dims<TIn, 64, 128>(a, st) : dkv_dims<TIn, 128, 128>(a, st));
   if (e != hipSuccess) return e;
   if (a.dq_part) {
     const int64_t n = pr.B * pr.T * pr.Hk * pr.Dk / 4, want = (n + 255) / 256;
