@@ -245,19 +245,20 @@ __device__ __forceinline__ void within_chunk(const bf16* Y, const bf16* Z, const
                                              const LaneOffsets<C, DX, DZ>& at, f16v (&S)[DX / 32],
                                              f16v (&acc)[C / 32]) {
   constexpr int RT = C / 32, KP = NP > 0 ? NP : 1, JS = C / 16;
-  bf8 z[2][PL], y[DX / 32], pf[RT][KP], piece[2][NS];
+  constexpr int YB = NP > 0 ? 1 : 2;  // without outputs there are registers for Y's reads a step ahead
+  bf8 z[2][PL], y[YB][DX / 32], pf[RT][KP], piece[2][NS];
   const int oy = fresh(at.y), oz = fresh(at.z), op = fresh(at.p);
   const auto inside = [](int rt, int js) { return REV ? js * 16 >= rt * 32 : js * 16 < rt * 32 + 32; };
-  const auto read_y = [&](int js, int pl) {
+  const auto read_y = [&](int i) {  // of step i / PL, plane i % PL
 #pragma unroll
-    for (int t = 0; t < DX / 32; ++t) y[t] = col_frag<DX>(Y + pl * C * DX, oy, js * 16, t * 32);
+    for (int t = 0; t < DX / 32; ++t) y[i % YB][t] = col_frag<DX>(Y + i % PL * C * DX, oy, i / PL * 16, t * 32);
   };
   const auto read_z = [&](int js) {
 #pragma unroll
     for (int pl = 0; pl < PL; ++pl) z[js & 1][pl] = col_frag<DZ>(Z + pl * C * DZ, oz, js * 16, 0);
   };
   read_z(0);
-  read_y(0, 0);
+  read_y(0);
   read_z(1);
   scale_state<DX / 32>(S, d.all);
   weigh<PL, NS>(z[0], d.in, 0, piece[0]);
@@ -273,17 +274,21 @@ __device__ __forceinline__ void within_chunk(const bf16* Y, const bf16* Z, const
         for (int p = 0; p < NP; ++p) pf[rt][p] = row_frag<C>(P + p * C * C, op, rt * 32, js * 16);
 #pragma unroll
     for (int pl = 0; pl < PL; ++pl) {
+      const int i = js * PL + pl;
       step_fence();
+      if (YB == 2 && i + 1 < JS * PL) {
+        read_y(i + 1);
+        step_fence();
+      }
 #pragma unroll
       for (int p = 0; p < NS; ++p)
         if (pl + p < NS)
 #pragma unroll
-          for (int t = 0; t < DX / 32; ++t) S[t] = mma32(y[t], piece[js & 1][p], S[t]);
+          for (int t = 0; t < DX / 32; ++t) S[t] = mma32(y[i % YB][t], piece[js & 1][p], S[t]);
       if (pl == 0 && js + 1 < JS) weigh<PL, NS>(z[(js + 1) & 1], d.in, js + 1, piece[(js + 1) & 1]);
       interleave<NS * (DX / 32), 6>();
       step_fence();
-      if (pl + 1 < PL) read_y(js, pl + 1);
-      else if (js + 1 < JS) read_y(js + 1, 0);
+      if (YB == 1 && i + 1 < JS * PL) read_y(i + 1);
     }
     step_fence();
 #pragma unroll
@@ -509,6 +514,36 @@ __device__ __forceinline__ float load_gate(const float* g, int64_t st, int t0, i
   return t < n ? g[(int64_t)t * st] : 0.f;
 }
 
+// The decays of a span's chunks, in the order they run (REV: from the last). A
+// prefix sum in 64 bits is a chain of a few hundred cycles: each of the WAVES
+// takes a chunk of its own, so that a workgroup waits for one such chain in WAVES
+// chunks, and g is read that far ahead.
+template <int C, int WAVES, bool REV>
+struct SpanDecays {
+  Decays<C>* dec;  // [WAVES], in LDS
+  const float* g;
+  int64_t st;
+  int wave, n, chunks, next = 0;
+  float scale, ahead = 0.f;
+  double total = 0.0;  // of the wave's chunks
+
+  __device__ __forceinline__ SpanDecays(Decays<C>* dec, const float* g, int64_t st, int n, float scale, int wave)
+      : dec(dec), g(g), st(st), wave(wave), n(n), chunks((n + C - 1) / C), scale(scale) {
+    read();
+  }
+  __device__ __forceinline__ void read() {
+    const int i = next + wave;
+    next += WAVES;
+    ahead = i < chunks ? load_gate(g, st, (REV ? chunks - 1 - i : i) * C, n) : 0.f;
+  }
+  // Those of the next WAVES chunks. Barriers on both sides: the last ones' must
+  // have been read, and these not yet be.
+  __device__ __forceinline__ void write() {
+    total += write_decays<C, REV>(dec[wave], ahead, scale);
+    read();
+  }
+};
+
 // Decay over a span and the state it adds, from a zero state: REV runs the
 // adjoint's recurrence. Not needed for the span that ends a sequence (REV: that
 // starts it), whose state nothing reads.
@@ -518,7 +553,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
   constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, DZ = NW * 32, NT = NW * 64;
   __shared__ __align__(16) bf16 Y[PL * C * DX];
   __shared__ __align__(16) bf16 Z[PL * C * DZ];
-  __shared__ __align__(16) Decays<C> dec;
+  __shared__ __align__(16) Decays<C> dec[NW];
+  __shared__ double sums[NW];
   const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
   const Span sp = find_span(pr, slot);
@@ -535,23 +571,21 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
   // loads run two chunks ahead: a chunk's own work is shorter than a load
   TileRegs<TIn, C, DX, NT> ry[2];
   TileRegs<TIn, C, DZ, NT> rz[2];
-  float rg[2] = {0.f, 0.f};
-  double total = 0.0;
+  SpanDecays<C, NW, REV> decays(dec, gp, pr.gst, sp.n, sz, wave);
   const LaneOffsets<C, DX, DZ> at(z0);
   f16v none[C / 32];
   const auto fetch = [&](int i, int s) {
     const int c = REV ? nc - 1 - i : i, t = c * C;
     ry[s].load(yp + (int64_t)t * y.st, y.st, y.d, sp.n - t);
     rz[s].load(zp + (int64_t)t * z.st, z.st, z.d, sp.n - t);
-    if (wave == 0) rg[s] = load_gate(gp, pr.gst, t, sp.n);
   };
   const auto chunk = [&](int i, int s) {
     ry[s].store(Y);
     rz[s].store(Z);
-    if (wave == 0) total += write_decays<C, REV>(dec, rg[s], sz);
+    if (i % NW == 0) decays.write();
     __syncthreads();
     if (i + 2 < nc) fetch(i + 2, s);
-    within_chunk<PL, C, DX, DZ, 0, REV>(Y, Z, nullptr, dec, at, S, none);
+    within_chunk<PL, C, DX, DZ, 0, REV>(Y, Z, nullptr, dec[i % NW], at, S, none);
     __syncthreads();
   };
   fetch(0, 0);
@@ -561,7 +595,13 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
     if (i + 1 < nc) chunk(i + 1, 1);
   }
   store_state<DX>(S, states + ((int64_t)slot * pr.H + h) * pr.Dk * pr.Dv, pr.Dv, 1, pr.Dk, pr.Dv, z0);
-  if (tid == 0) totals[(int64_t)slot * pr.H + h] = exp2_fast((float)total);
+  if (lane_id() == 0) sums[wave] = decays.total;
+  __syncthreads();
+  if (tid == 0) {
+    double total = 0.0;
+    for (int w = 0; w < NW; ++w) total += sums[w];
+    totals[(int64_t)slot * pr.H + h] = exp2_fast((float)total);
+  }
 }
 
 }  // namespace la

@@ -19,7 +19,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   __shared__ __align__(16) bf16 K[PL * C * DX];
   __shared__ __align__(16) bf16 V[PL * C * DZ];
   __shared__ __align__(16) bf16 P[NP * C * C];
-  __shared__ __align__(16) Decays<C> dec[2];
+  __shared__ __align__(16) Decays<C> dec[NW];
   const LaProblem& pr = a.pr;
   const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
@@ -42,13 +42,10 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   const float* gp = gate_base(pr, sp.batch, sp.t0, h);
   TileRegs<TIn, C, DX, NT> rq, rk;
   TileRegs<TIn, C, DZ, NT> rv;
-  float rg = 0.f;
+  SpanDecays<C, NW, false> decays(dec, gp, pr.gst, sp.n, pr.scale, wave);
   // the next chunk's loads are issued in three places: all at once they hold up
   // the waves for as long as the memory pipeline takes to accept them
-  const auto fetch_q = [&](int t) {
-    rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t);
-    if (wave == NW - 1) rg = load_gate(gp, pr.gst, t, sp.n);
-  };
+  const auto fetch_q = [&](int t) { rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t); };
   const auto fetch_k = [&](int t) { rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t); };
   const auto fetch_v = [&](int t) { rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t); };
   const LaneOffsets<C, DX, DZ> at(z0);
@@ -59,11 +56,11 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
     rq.store(Q);
     rk.store(K);
     rv.store(V);
-    if (wave == NW - 1) write_decays<C, false>(dec[0], rg, pr.scale);
+    decays.write();
   }
   settle();
   __syncthreads();
-  for (int t = 0, cur = 0; t < sp.n; t += C, cur ^= 1) {
+  for (int t = 0, cur = 0; t < sp.n; t += C) {
     const bool more = t + C < sp.n;
     if (more) fetch_q(t + C);
     scores<PL, C, DX, NP, false, NW>(Q, K, at.x16, P, dec[cur], pr.scale, wave);
@@ -74,7 +71,6 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
     scale_rows<C>(acc, dec[cur].out);
     __syncthreads();
     within_chunk<PL, C, DX, DZ, NP, false>(K, V, P, dec[cur], at, S, acc);
-    if (more && wave == NW - 1) write_decays<C, false>(dec[cur ^ 1], rg, pr.scale);
     rows_to_lds<TIn, C, DZ>(acc, (TIn*)Q, z0);
     __syncthreads();
     OutRegs<TIn, C, DZ, NT> out;
@@ -84,6 +80,10 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
       rq.store(Q);
       rk.store(K);
       rv.store(V);
+      if (++cur == NW) {
+        cur = 0;
+        decays.write();
+      }
     }
     out.put(op + t * ost, ost, sp.n - t, pr.Dv);
     __syncthreads();

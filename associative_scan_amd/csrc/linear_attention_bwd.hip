@@ -36,7 +36,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   __shared__ __align__(16) bf16 V[PL * C * DX];
   __shared__ __align__(16) bf16 K[PL * C * DZ];
   __shared__ __align__(16) bf16 P[NP * C * C];
-  __shared__ __align__(16) Decays<C> dec[2];
+  __shared__ __align__(16) Decays<C> dec[NW];
   __shared__ float part[NW][C];
   const LaProblem& pr = a.pr;
   const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
@@ -66,11 +66,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   const float* gp = gate_base(pr, sp.batch, sp.t0, h);
   TileRegs<TIn, C, DX, NT> ro, rv;
   TileRegs<TIn, C, DZ, NT> rk;
-  float rg = 0.f;
-  const auto fetch_o = [&](int t) {
-    ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t);
-    if (wave == NW - 1) rg = load_gate(gp, pr.gst, t, sp.n);
-  };
+  SpanDecays<C, NW, false> decays(dec, gp, pr.gst, sp.n, pr.scale, wave);
+  const auto fetch_o = [&](int t) { ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t); };
   const auto fetch_v = [&](int t) { rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t); };
   const auto fetch_k = [&](int t) { rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t); };
   const LaneOffsets<C, DX, DZ> at(z0);
@@ -80,10 +77,10 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   ro.store(O);
   rv.store(V);
   rk.store(K);
-  if (wave == NW - 1) write_decays<C, false>(dec[0], rg, pr.scale);
+  decays.write();
   settle();
   __syncthreads();
-  for (int t = 0, cur = 0; t < sp.n; t += C, cur ^= 1) {
+  for (int t = 0, cur = 0; t < sp.n; t += C) {
     const bool more = t + C < sp.n;
     RowRegs<TIn, C> rq;
     if constexpr (DG) rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t, z0);
@@ -108,7 +105,6 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
     OutRegs<TIn, C, DZ, NT> out;
     if (shared) store_rows<float, C>(acc, a.dq_part + o, ost, sp.n - t, pr.Dk, z0);
     else rows_to_lds<TIn, C, DZ>(acc, (TIn*)O, z0);
-    if (more && wave == NW - 1) write_decays<C, false>(dec[cur ^ 1], rg, pr.scale);
     __syncthreads();
     if (!shared) out.take((const TIn*)O);
     if constexpr (DX != DZ || PL != 1) __syncthreads();
@@ -116,6 +112,10 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
       ro.store(O);
       rv.store(V);
       rk.store(K);
+      if (++cur == NW) {
+        cur = 0;
+        decays.write();
+      }
     }
     if (!shared) out.put((TIn*)a.dq + o, ost, sp.n - t, pr.Dk);
     __syncthreads();
@@ -148,7 +148,7 @@ struct DkvTiles {
   bf16 V[PL * C * DV];  // and then the chunk's dv
   bf16 O[PL * C * DV];
   bf16 P[2][kPiecesP<TIn> * C * C];
-  Decays<C> dec[2];
+  Decays<C> dec[(DK + DV) / 32];
   float part[DK / 32][C];
   float sums[kTiles<C>][2][16];
 };
@@ -182,12 +182,8 @@ __device__ __forceinline__ void dkv_span(const BwdArgs& a, const Span& sp, int s
   const TIn* p2 = head_base<TIn>(h2, sp.batch, sp.t0, h);
   const float* gp = gate_base(pr, sp.batch, sp.t0, h);
   TileRegs<TIn, C, DZ, NT> r1, r2;
-  float rg = 0.f;
-  const bool decays = !IS_DK && wave == 0;  // this wave's work besides
-  const auto fetch1 = [&](int t) {
-    r1.load(p1 + (int64_t)t * h1.st, h1.st, dz, sp.n - t);
-    if (decays) rg = load_gate(gp, pr.gst, t, sp.n);
-  };
+  SpanDecays<C, NW, true> decays(sh.dec, gp, pr.gst, sp.n, pr.scale, wave);
+  const auto fetch1 = [&](int t) { r1.load(p1 + (int64_t)t * h1.st, h1.st, dz, sp.n - t); };
   const auto fetch2 = [&](int t) { r2.load(p2 + (int64_t)t * h2.st, h2.st, dz, sp.n - t); };
   const LaneOffsets<C, DX, DZ> at(z0);
   const int k16 = row_lane<DK, 16>(), v16 = row_lane<DV, 16>();
@@ -197,11 +193,11 @@ __device__ __forceinline__ void dkv_span(const BwdArgs& a, const Span& sp, int s
     fetch2(last);
     r1.store(T1);
     r2.store(T2);
-    if (decays) write_decays<C, true>(sh.dec[0], rg, pr.scale);
+    decays.write();
   }
   settle();
   __syncthreads();
-  for (int t = last, cur = 0; t >= 0; t -= C, cur ^= 1) {
+  for (int t = last, cur = 0; t >= 0; t -= C) {
     const bool more = t > 0;
     if (more) fetch1(t - C);
     {  // scores of both roles, and W's sums over i and over j
@@ -266,7 +262,6 @@ __device__ __forceinline__ void dkv_span(const BwdArgs& a, const Span& sp, int s
     const int64_t ost = (int64_t)pr.H * dz, o = row0 * dz + (int64_t)t * ost;
     if (shared) store_rows<float, C>(acc, a.dk_part + o, ost, sp.n - t, dz, z0);
     else rows_to_lds<TIn, C, DZ>(acc, (TIn*)T1, z0);
-    if (more && decays) write_decays<C, true>(sh.dec[cur ^ 1], rg, pr.scale);
     __syncthreads();
     OutRegs<TIn, C, DZ, NT> out;
     if (!shared) out.take((const TIn*)T1);
@@ -274,6 +269,10 @@ __device__ __forceinline__ void dkv_span(const BwdArgs& a, const Span& sp, int s
     if (more) {
       r1.store(T1);
       r2.store(T2);
+      if (++cur == NW) {
+        cur = 0;
+        decays.write();
+      }
     }
     if (!shared) out.put((TIn*)(IS_DK ? a.dk : a.dv) + o, ost, sp.n - t, dz);
     __syncthreads();
