@@ -86,7 +86,7 @@ FwdSpace fwd_space(const LaProblem& r) {
 
 // Offsets of the backward's workspace.
 struct BwdSpace {
-  size_t states = 0, lams = 0, totals = 0, dq_part = 0, dk_part = 0, rows = 0, dg_part = 0, bytes = 0;
+  size_t states = 0, lams = 0, totals = 0, ltotals = 0, dq_part = 0, dk_part = 0, rows = 0, dg_part = 0, bytes = 0;
 };
 BwdSpace bwd_space(const LaProblem& r) {
   BwdSpace w;
@@ -100,6 +100,7 @@ BwdSpace bwd_space(const LaProblem& r) {
   w.states = take(split ? cells : 0);
   w.lams = take(split ? cells : 0);
   w.totals = take(split ? (size_t)r.slots * r.H * 4 : 0);
+  w.ltotals = take(split ? (size_t)r.slots * r.H * 4 : 0);
   const size_t part = r.H != r.Hk ? tokens * r.H * r.Dk * 4 : 0;
   w.dq_part = take(part);
   w.dk_part = take(part);
@@ -212,6 +213,7 @@ mscan_status linear_attention_bwd(const mscan_attention* prob, int dtype, const 
   a.states = (float*)(base + w.states);
   a.lams = (float*)(base + w.lams);
   a.totals = (float*)(base + w.totals);
+  a.ltotals = (float*)(base + w.ltotals);
   a.dq_part = share > 1 ? (float*)(base + w.dq_part) : nullptr;
   a.dk_part = share > 1 ? (float*)(base + w.dk_part) : nullptr;
   a.rows = (float*)(base + w.rows);

@@ -547,14 +547,18 @@ struct SpanDecays {
 // Decay over a span and the state it adds, from a zero state: REV runs the
 // adjoint's recurrence. Not needed for the span that ends a sequence (REV: that
 // starts it), whose state nothing reads.
+template <class TIn, int DX, int NW>
+struct SpanTiles {
+  static constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>;
+  bf16 Y[PL * C * DX];
+  bf16 Z[PL * C * NW * 32];
+  Decays<C> dec[NW];
+  double sums[NW];
+};
 template <class TIn, int DX, int NW, bool REV>
-__global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, const Heads y, const Heads z, float sz,
-                                                            float* states, float* totals) {
+__device__ __forceinline__ void span_state(const LaProblem& pr, const Between& a, SpanTiles<TIn, DX, NW>& sh) {
   constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, DZ = NW * 32, NT = NW * 64;
-  __shared__ __align__(16) bf16 Y[PL * C * DX];
-  __shared__ __align__(16) bf16 Z[PL * C * DZ];
-  __shared__ __align__(16) Decays<C> dec[NW];
-  __shared__ double sums[NW];
+  const Heads &y = a.y, &z = a.z;
   const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
   const Span sp = find_span(pr, slot);
@@ -571,7 +575,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
   // loads run two chunks ahead: a chunk's own work is shorter than a load
   TileRegs<TIn, C, DX, NT> ry[2];
   TileRegs<TIn, C, DZ, NT> rz[2];
-  SpanDecays<C, NW, REV> decays(dec, gp, pr.gst, sp.n, sz, wave);
+  SpanDecays<C, NW, REV> decays(sh.dec, gp, pr.gst, sp.n, a.sz, wave);
   const LaneOffsets<C, DX, DZ> at(z0);
   f16v none[C / 32];
   const auto fetch = [&](int i, int s) {
@@ -580,12 +584,12 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
     rz[s].load(zp + (int64_t)t * z.st, z.st, z.d, sp.n - t);
   };
   const auto chunk = [&](int i, int s) {
-    ry[s].store(Y);
-    rz[s].store(Z);
+    ry[s].store(sh.Y);
+    rz[s].store(sh.Z);
     if (i % NW == 0) decays.write();
     __syncthreads();
     if (i + 2 < nc) fetch(i + 2, s);
-    within_chunk<PL, C, DX, DZ, 0, REV>(Y, Z, nullptr, dec[i % NW], at, S, none);
+    within_chunk<PL, C, DX, DZ, 0, REV>(sh.Y, sh.Z, nullptr, sh.dec[i % NW], at, S, none);
     __syncthreads();
   };
   fetch(0, 0);
@@ -594,14 +598,20 @@ __global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, 
     chunk(i, 0);
     if (i + 1 < nc) chunk(i + 1, 1);
   }
-  store_state<DX>(S, states + ((int64_t)slot * pr.H + h) * pr.Dk * pr.Dv, pr.Dv, 1, pr.Dk, pr.Dv, z0);
-  if (lane_id() == 0) sums[wave] = decays.total;
+  store_state<DX>(S, a.states + ((int64_t)slot * pr.H + h) * pr.Dk * pr.Dv, pr.Dv, 1, pr.Dk, pr.Dv, z0);
+  if (lane_id() == 0) sh.sums[wave] = decays.total;
   __syncthreads();
   if (tid == 0) {
     double total = 0.0;
-    for (int w = 0; w < NW; ++w) total += sums[w];
-    totals[(int64_t)slot * pr.H + h] = exp2_fast((float)total);
+    for (int w = 0; w < NW; ++w) total += sh.sums[w];
+    a.totals[(int64_t)slot * pr.H + h] = exp2_fast((float)total);
   }
+}
+template <class TIn, int DX, int NW>
+__global__ __launch_bounds__(NW * 64, 2) void k_span_states(const LaProblem pr, const Between fwd, const Between adj) {
+  __shared__ __align__(16) SpanTiles<TIn, DX, NW> sh;
+  if (blockIdx.y == 0) span_state<TIn, DX, NW, false>(pr, fwd, sh);
+  else span_state<TIn, DX, NW, true>(pr, adj, sh);
 }
 
 }  // namespace la

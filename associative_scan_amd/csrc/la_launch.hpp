@@ -33,11 +33,16 @@ struct LaProblem {
 void plan(LaProblem& p, int dtype, bool backward);
 
 // The states between spans: what each span adds (see k_span_states), and from
-// these the states at the spans' starts (rev: the adjoint's at their ends).
-hipError_t launch_span_states(const LaProblem& p, int dtype, bool rev, const Heads& y, const Heads& z, float sz,
-                              float* states, float* totals, hipStream_t st);
-hipError_t launch_join(const LaProblem& p, bool rev, const float* outer, float* states, const float* totals,
-                       hipStream_t st);
+// these the states at the spans' starts (the adjoint's: at their ends).
+struct Between {
+  Heads y, z;          // S += y^T (sz z)
+  float sz;
+  const float* outer;  // [N][H][Dk][Dv]: what comes before the first span (adjoint: behind the last), or null
+  float* states;       // [slots][H][Dk][Dv]
+  float* totals;       // [slots][H], the decay over a span
+};
+// One direction, or (adj not null) both at a time.
+hipError_t launch_between(const LaProblem& p, int dtype, const Between& fwd, const Between* adj, hipStream_t st);
 
 struct FwdArgs {
   LaProblem pr;
@@ -74,7 +79,7 @@ struct BwdArgs {
   float* dh0;          // or null
   // workspace
   float *states, *totals;   // as in FwdArgs (split problems)
-  float *lams;              // split problems: the adjoint state after each span
+  float *lams, *ltotals;    // split problems: the adjoint state after each span
   float *dq_part, *dk_part; // shared heads: [B][T][H][Dk] each
   float* rows;              // dg: [2][B][T][H], and one value per (slot, head) behind them
   double* dg_part;          // dg_sum: [slots][H]

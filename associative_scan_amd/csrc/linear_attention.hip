@@ -93,11 +93,13 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
 }
 
 // The states between the spans of a sequence: states[slot] holds what a span
-// adds and becomes what the recurrence brings to its start (REV: to its end,
+// adds and becomes what the recurrence brings to its start (adjoint: to its end,
 // from the last span to the first).
-template <bool REV>
-__global__ __launch_bounds__(256) void k_join(const LaProblem pr, const float* outer, float* states,
-                                              const float* totals) {
+__global__ __launch_bounds__(256) void k_join(const LaProblem pr, const Between fwd, const Between adj) {
+  const bool rev = blockIdx.y != 0;
+  const float* outer = rev ? adj.outer : fwd.outer;
+  float* states = rev ? adj.states : fwd.states;
+  const float* totals = rev ? adj.totals : fwd.totals;
   const int64_t cells = (int64_t)pr.Dk * pr.Dv;
   const int parts = (int)((cells / 4 + 255) / 256);
   const int part = blockIdx.x % parts, h = blockIdx.x / parts % pr.H, seq = blockIdx.x / parts / pr.H;
@@ -122,29 +124,18 @@ __global__ __launch_bounds__(256) void k_join(const LaProblem pr, const float* o
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (c0 + i < n - 1) {
-        const int64_t slot = first + (REV ? n - 1 - (c0 + i) : c0 + i);
+        const int64_t slot = first + (rev ? n - 1 - (c0 + i) : c0 + i);
         add[i] = *(const f4v*)(states + (slot * pr.H + h) * cells + at);
         f[i] = totals[slot * pr.H + h];
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       if (c0 + i < n) {
-        const int64_t slot = first + (REV ? n - 1 - (c0 + i) : c0 + i);
+        const int64_t slot = first + (rev ? n - 1 - (c0 + i) : c0 + i);
         *(f4v*)(states + (slot * pr.H + h) * cells + at) = S;
         if (c0 + i < n - 1) S = S * f[i] + add[i];
       }
   }
-}
-
-hipError_t launch_join(const LaProblem& p, bool rev, const float* outer, float* states, const float* totals,
-                       hipStream_t st) {
-  const int64_t cells = (int64_t)p.Dk * p.Dv;
-  const int64_t blocks = (cells / 4 + 255) / 256 * p.H * (p.cu ? p.nseg : p.B);
-  if (rev)
-    hipLaunchKernelGGL((k_join<true>), dim3((unsigned)blocks), dim3(256), 0, st, p, outer, states, totals);
-  else
-    hipLaunchKernelGGL((k_join<false>), dim3((unsigned)blocks), dim3(256), 0, st, p, outer, states, totals);
-  return hipGetLastError();
 }
 
 // Steps per span. A workgroup per head and sequence needs no second pass over
@@ -190,31 +181,27 @@ void plan(LaProblem& p, int dtype, bool backward) {
 }
 
 template <class TIn, int DX, int NW>
-static hipError_t states_dims(const LaProblem& p, bool rev, const Heads& y, const Heads& z, float sz, float* states,
-                              float* totals, hipStream_t st) {
+static hipError_t states_dims(const LaProblem& p, const Between& fwd, const Between& adj, int dirs, hipStream_t st) {
   const unsigned blocks = (unsigned)((int64_t)p.slots * p.H);
-  if (rev)
-    hipLaunchKernelGGL((k_span_states<TIn, DX, NW, true>), dim3(blocks), dim3(NW * 64), 0, st, p, y, z, sz, states,
-                       totals);
-  else
-    hipLaunchKernelGGL((k_span_states<TIn, DX, NW, false>), dim3(blocks), dim3(NW * 64), 0, st, p, y, z, sz,
-                       states, totals);
+  hipLaunchKernelGGL((k_span_states<TIn, DX, NW>), dim3(blocks, dirs), dim3(NW * 64), 0, st, p, fwd, adj);
   return hipGetLastError();
 }
 template <class TIn>
-static hipError_t states_type(const LaProblem& p, bool rev, const Heads& y, const Heads& z, float sz, float* states,
-                              float* totals, hipStream_t st) {
+static hipError_t states_type(const LaProblem& p, const Between& fwd, const Between& adj, int dirs, hipStream_t st) {
   if (p.Dk <= 64)
-    return p.Dv <= 64 ? states_dims<TIn, 64, 2>(p, rev, y, z, sz, states, totals, st)
-                      : states_dims<TIn, 64, 4>(p, rev, y, z, sz, states, totals, st);
-  return p.Dv <= 64 ? states_dims<TIn, 128, 2>(p, rev, y, z, sz, states, totals, st)
-                    : states_dims<TIn, 128, 4>(p, rev, y, z, sz, states, totals, st);
+    return p.Dv <= 64 ? states_dims<TIn, 64, 2>(p, fwd, adj, dirs, st) : states_dims<TIn, 64, 4>(p, fwd, adj, dirs, st);
+  return p.Dv <= 64 ? states_dims<TIn, 128, 2>(p, fwd, adj, dirs, st) : states_dims<TIn, 128, 4>(p, fwd, adj, dirs, st);
 }
-hipError_t launch_span_states(const LaProblem& p, int dtype, bool rev, const Heads& y, const Heads& z, float sz,
-                              float* states, float* totals, hipStream_t st) {
-  if (dtype == 0) return states_type<float>(p, rev, y, z, sz, states, totals, st);
-  if (dtype == 1) return states_type<__bf16>(p, rev, y, z, sz, states, totals, st);
-  return states_type<_Float16>(p, rev, y, z, sz, states, totals, st);
+hipError_t launch_between(const LaProblem& p, int dtype, const Between& fwd, const Between* adj, hipStream_t st) {
+  const int dirs = adj ? 2 : 1;
+  const Between& back = adj ? *adj : fwd;
+  const hipError_t e = dtype == 0   ? states_type<float>(p, fwd, back, dirs, st)
+                       : dtype == 1 ? states_type<__bf16>(p, fwd, back, dirs, st)
+                                    : states_type<_Float16>(p, fwd, back, dirs, st);
+  if (e != hipSuccess) return e;
+  const int64_t cells = (int64_t)p.Dk * p.Dv, blocks = (cells / 4 + 255) / 256 * p.H * (p.cu ? p.nseg : p.B);
+  hipLaunchKernelGGL(k_join, dim3((unsigned)blocks, dirs), dim3(256), 0, st, p, fwd, back);
+  return hipGetLastError();
 }
 
 template <class TIn, int DX, int NW>
@@ -235,9 +222,9 @@ static hipError_t fwd_type(const FwdArgs& a, hipStream_t st) {
 
 hipError_t launch_fwd(const FwdArgs& a, int dtype, hipStream_t st) {
   if (a.pr.T > a.pr.span) {
-    hipError_t e = launch_span_states(a.pr, dtype, false, a.k, a.v, 1.f, a.states, a.totals, st);
+    const Between fwd{a.k, a.v, 1.f, a.h0, a.states, a.totals};
+    const hipError_t e = launch_between(a.pr, dtype, fwd, nullptr, st);
     if (e != hipSuccess) return e;
-    if ((e = launch_join(a.pr, false, a.h0, a.states, a.totals, st)) != hipSuccess) return e;
   }
   if (dtype == 0) return fwd_type<float>(a, st);
   if (dtype == 1) return fwd_type<__bf16>(a, st);

@@ -402,10 +402,8 @@ static hipError_t bwd_type(const BwdArgs& a, int dtype, hipStream_t st) {
   const LaProblem& pr = a.pr;
   hipError_t e;
   if (pr.T > pr.span) {
-    if ((e = launch_span_states(pr, dtype, false, a.k, a.v, 1.f, a.states, a.totals, st)) != hipSuccess) return e;
-    if ((e = launch_join(pr, false, a.h0, a.states, a.totals, st)) != hipSuccess) return e;
-    if ((e = launch_span_states(pr, dtype, true, a.q, a.dO, pr.scale, a.lams, a.totals, st)) != hipSuccess) return e;
-    if ((e = launch_join(pr, true, a.dht, a.lams, a.totals, st)) != hipSuccess) return e;
+    const Between fwd{a.k, a.v, 1.f, a.h0, a.states, a.totals}, adj{a.q, a.dO, pr.scale, a.dht, a.lams, a.ltotals};
+    if ((e = launch_between(pr, dtype, fwd, &adj, st)) != hipSuccess) return e;
   }
   const bool k64 = pr.Dk <= 64, v64 = pr.Dv <= 64;
   e = v64 ? (k64 ? dq_dims<TIn, 64, 2>(a, st) : dq_dims<TIn, 64, 4>(a, st))
