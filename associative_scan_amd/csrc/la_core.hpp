@@ -546,7 +546,9 @@ struct SpanDecays {
 
 // Decay over a span and the state it adds, from a zero state: REV runs the
 // adjoint's recurrence. Not needed for the span that ends a sequence (REV: that
-// starts it), whose state nothing reads.
+// starts it), whose state nothing reads. The loads of two chunks are on their way
+// while a third is worked on; without them the rest takes 80 % of the time, without
+// the products 60 %.
 template <class TIn, int DX, int NW>
 struct SpanTiles {
   static constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>;

@@ -132,8 +132,9 @@ __device__ __forceinline__ f8v widen(bf8 f) { return __builtin_convertvector(f, 
 // and l + 32 of a 32-wide tile take entries 8 h .. 8 h + 7, h = l / 32, of a
 // 16-step. An accumulator of a state holds, in 8 consecutive registers, rows
 // 8 e + 4 h + i (e < 2, i < 4) of 16; the state's rows are numbered so that these
-// are its entries 8 h + 4 e + i (state_row), which makes a state kept in
-// accumulators an operand without a move between lanes.
+// are its entries 8 h + 4 e + i: accumulator row m is entry m with bits 2 and 3
+// exchanged, which makes a state kept in accumulators an operand without a move
+// between lanes.
 // ---------------------------------------------------------------------------
 __device__ __forceinline__ f16v mma32(bf8 a, bf8 b, f16v c) {
   return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
@@ -189,13 +190,9 @@ template <int D>
 __device__ __forceinline__ bf8 row_frag(const bf16* tile, int off, int row0, int k0) {
   return *(const bf8*)(tile + moved<bf16, D>(off, row0, k0 / 8));
 }
-// Entry of a state's 32 rows that row m of its accumulators holds: bits 2 and 3
-// change places.
-__device__ __forceinline__ constexpr int state_row(int m) { return (m & ~12) | ((m & 4) << 1) | ((m & 8) >> 1); }
-
 // Column fragments: 32-wide tiles, contraction axis down the rows row0 + 8 h ..
 // + 7, row0 a multiple of 16. Columns col0 (a multiple of 32) + l % 32, or, as
-// rows of a state (STATE), col0 + state_row(l % 32). A transposing read: each 16
+// rows of a state (STATE), col0 + the entry of accumulator row l % 32. A transposing read: each 16
 // lanes read 4 rows x 16 columns, lane i of them 8 bytes of row i / 4, and get
 // column i of the four rows.
 template <int D, bool STATE>

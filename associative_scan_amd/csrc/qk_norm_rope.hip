@@ -10,6 +10,10 @@
 // shares its angle; 16 lanes still read 128 contiguous bytes at a time. A lane
 // group takes several heads of a token and reads the token's angles once. Loads
 // and stores are streaming: they pass the caches by for inputs that come back.
+// Measured in bf16, D = 128: forward, 32767 tokens of 16 + 4 heads 76 us (4.5
+// TB/s), forward and backward, 32768 tokens of 12 + 12 heads 191 us (5.3 TB/s; a
+// copy reaches 5.35); a decoding step of 7 tokens 4.4 us, its three dependent trips
+// to memory.
 #include "la_device.hpp"
 #include "qk_norm_rope.hpp"
 
