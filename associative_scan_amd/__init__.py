@@ -650,7 +650,11 @@ def linear_attention(q, k, v, g, h0=None, cu_seqlens=None, scale=None):
 def qk_norm_rope(q, k, q_weight=None, k_weight=None, cos=None, sin=None, positions=None, eps=1e-6, interleaved=False):
     """Differentiable RMS norm of queries and keys for each head with the position
     rotation (qk_norm_rope_fwd), with native kernels for the gradients of q, k and
-    the weights."""
+    the weights. cos and sin are constants."""
+    if torch.is_grad_enabled():
+        for t, name in ((cos, "cos"), (sin, "sin")):
+            if t is not None and t.requires_grad:
+                raise ValueError(f"{name} gets no gradient: pass it without requires_grad")
     return torch.ops.mscan.qk_norm_rope(q, k, q_weight, k_weight, cos, sin, positions, eps, interleaved)
 
 
@@ -668,7 +672,7 @@ def rotary_linear_attention_step(q, k, v, g, state, q_weight=None, k_weight=None
                                  slots=None, scale=None, eps=1e-6, interleaved=False):
     """One token of rotary_linear_attention for each sequence, q, k [B, Hk, Dk],
     against a pool of states updated in place (linear_attention_step).
-    positions: [B], the tokens' positions."""
+    positions: [B], the tokens' positions (default: all at 0)."""
     q, k = torch.ops.mscan.qk_norm_rope(q[:, None], k[:, None], q_weight, k_weight, cos, sin,
                                         None if positions is None else positions[:, None], eps, interleaved)
     return torch.ops.mscan.linear_attention_step(q[:, 0], k[:, 0], v, g, state, slots,

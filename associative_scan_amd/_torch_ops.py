@@ -202,6 +202,12 @@ def _grad_rows(t: Optional[Tensor], like: Tensor) -> Tensor:
     return t.contiguous()
 
 
+def _aligned(t: Optional[Tensor]) -> Optional[Tensor]:
+    """An incoming gradient may start anywhere in its storage (what torch.cat gives
+    back is a slice of its own gradient); the kernels read 16 bytes at a time."""
+    return t if t is None or t.data_ptr() % 16 == 0 else t.clone()
+
+
 @torch.library.custom_op("mscan::linear_attention", mutates_args=())
 def linear_attention_op(q: Tensor, k: Tensor, v: Tensor, g: Tensor, h0: Optional[Tensor],
                         cu_seqlens: Optional[Tensor], scale: float) -> Tuple[Tensor, Tensor]:
@@ -217,8 +223,8 @@ def _(q, k, v, g, h0, cu_seqlens, scale):
 def linear_attention_backward_op(q: Tensor, k: Tensor, v: Tensor, g: Tensor, do: Tensor, h0: Optional[Tensor],
                                  dht: Optional[Tensor], cu_seqlens: Optional[Tensor], scale: float, need_dg: bool,
                                  need_dh0: bool) -> Tuple[Tensor, Tensor, Tensor, Tensor, Tensor]:
-    dq, dk, dv, dg, dh0 = linear_attention_bwd(q, k, v, g, do, h0=h0, dht=dht, cu_seqlens=cu_seqlens, scale=scale,
-                                               need_dg=need_dg, need_dh0=need_dh0)
+    dq, dk, dv, dg, dh0 = linear_attention_bwd(q, k, v, g, _aligned(do), h0=h0, dht=_aligned(dht), cu_seqlens=cu_seqlens,
+                                               scale=scale, need_dg=need_dg, need_dh0=need_dh0)
     return dq, dk, dv, dg if need_dg else _nothing(g), dh0 if need_dh0 else _nothing(g)
 
 
@@ -280,8 +286,8 @@ def qk_norm_rope_backward_op(q: Tensor, k: Tensor, q_weight: Optional[Tensor], k
                              cos: Optional[Tensor], sin: Optional[Tensor], dyq: Tensor, dyk: Tensor,
                              positions: Optional[Tensor], eps: float, interleaved: bool,
                              need_dw: bool) -> Tuple[Tensor, Tensor, Tensor, Tensor]:
-    dq, dk, dwq, dwk = qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, dyq, dyk, positions=positions, eps=eps,
-                                        interleaved=interleaved, need_dw=need_dw)
+    dq, dk, dwq, dwk = qk_norm_rope_bwd(q, k, q_weight, k_weight, cos, sin, _aligned(dyq), _aligned(dyk), positions=positions,
+                                        eps=eps, interleaved=interleaved, need_dw=need_dw)
     return dq, dk, _nothing(q) if dwq is None else dwq, _nothing(k) if dwk is None else dwk
 
 

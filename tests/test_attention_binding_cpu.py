@@ -235,3 +235,10 @@ def test_ops_are_registered_with_fake_kernels(m):
     assert y.shape == (50, 4, 24)
     a, b = torch.ops.mscan.qk_norm_rope(q, k, None, None, None, None, None, 1e-6, False)
     assert a.shape == q.shape and b.dtype == k.dtype
+
+
+def test_tables_get_no_gradient(m):
+    q, t = torch.zeros(1, 2, 1, 16), torch.zeros(4, 8)
+    for cos, sin, name in ((t.clone().requires_grad_(), t, "cos"), (t, t.clone().requires_grad_(), "sin")):
+        with pytest.raises(ValueError, match=name):
+            m.qk_norm_rope(q, q, cos=cos, sin=sin)

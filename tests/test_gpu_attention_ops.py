@@ -271,3 +271,30 @@ def test_two_streams_at_once(m):
         for g, w in zip(got, want):
             for a, b in zip(g, w):
                 assert torch.equal(a, b)
+
+
+def test_gradients_that_start_anywhere(m):
+    """Outputs that went through torch.cat: their gradients are contiguous slices
+    that start 2 or 4 bytes into 16."""
+    def through_cat(*outs):
+        loss, parts = 0.0, []
+        for t in outs:
+            w = torch.randn(t.numel() + 1, device=DEV).to(t.dtype)
+            loss = loss + (torch.cat([t.new_zeros(1), t.reshape(-1)]) * w).float().sum()
+            parts.append(w[1:].reshape(t.shape).clone())
+        return loss, parts
+
+    for dtype in (torch.bfloat16, torch.float32):
+        x = [t.requires_grad_() for t in make(30, 1, 20, 2, 16, 8, dtype)]
+        loss, (do, dht) = through_cat(*m.linear_attention(*x[:4], h0=x[4], scale=0.3))
+        got = torch.autograd.grad(loss, x)
+        want = m.linear_attention_bwd(*(t.detach() for t in x[:4]), do, h0=x[4].detach(), dht=dht, scale=0.3)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+        cos, sin = tables(20, 16)
+        w = torch.rand(16, device=DEV)
+        loss, dy = through_cat(*m.qk_norm_rope(x[0], x[1], w, w, cos, sin))
+        got = torch.autograd.grad(loss, x[:2])
+        want = m.qk_norm_rope_bwd(x[0].detach(), x[1].detach(), w, w, cos, sin, *dy)
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)

@@ -331,3 +331,54 @@ def test_backward_strides(m):
     ones = torch.ones(1, 1, 1, 32, device=DEV, dtype=q.dtype).expand(2, 140, 4, 32)
     for a, b in zip(m.linear_attention_bwd(q, k, v, g, ones), m.linear_attention_bwd(q, k, v, g, ones.contiguous())):
         assert torch.equal(a, b)
+
+
+# ---------------------------------------------------------------------------
+# long spans and far addresses
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("Dk,Dv", [(8, 8), (16, 72), (72, 16), (72, 72)])
+def test_many_chunks_of_one_workgroup(m, Dk, Dv, dtype):
+    """So many sequences and heads that none is cut: each workgroup runs more chunks
+    than it has waves. The first and the last sequence are compared."""
+    x = make(9, 65, 700, 8, Dk, Dv, dtype, spread=(3.0, 9.0))
+    q, k, v, g, h0, do, dht = x
+    got = m.linear_attention_fwd(q, k, v, g, h0=h0) + m.linear_attention_bwd(q, k, v, g, do, h0=h0, dht=dht)
+    pick = torch.tensor([0, 64], device=DEV)
+    some = [f64(t[pick]) for t in x]
+    sc = Dk ** -0.5
+    want = ref.forward(*some[:4], some[4], None, sc) + ref.backward(*some[:4], some[5], some[4], some[6], None, sc)
+    rows = (np.abs(some[0]) * want[2][1]).sum(3) + (np.abs(some[1]) * want[3][1]).sum(3)
+    want[5][1][:] += 700 ** 0.5 * rows.max(1, keepdims=True)
+    for n, a, w in zip(("o", "ht", "dq", "dk", "dv", "dg", "dh0"), got, want):
+        close(a[pick], w, n, 700, Dk, Dv, dtype)
+
+
+def test_offsets_past_32_bits(m):
+    """Values and outputs of more than 2^31 elements: the last sequence of a packed
+    row against the same steps by themselves."""
+    T, n, H, Dk, Dv = 2 ** 18 + 100, 100, 64, 8, 128
+    assert (T - n) * H * Dv >= 2 ** 31
+    x = make(10, 1, n, H, Dk, Dv, Hk=1, n=1)
+    q, k, v, g, h0, do, dht = x
+
+    def far(t):
+        out = torch.zeros((1, T) + t.shape[2:], dtype=t.dtype, device=DEV)
+        out[:, T - n:] = t
+        return out
+
+    cu = torch.tensor([0, T - n, T], dtype=torch.int32, device=DEV)
+    states = torch.cat([torch.zeros_like(h0), h0]), torch.cat([torch.zeros_like(dht), dht])
+    far_x = [far(t) for t in (q, k, v, g, do)]
+    o, ht = m.linear_attention_fwd(*far_x[:4], h0=states[0], cu_seqlens=cu)
+    grads = m.linear_attention_bwd(*far_x, h0=states[0], dht=states[1], cu_seqlens=cu)
+    sc = Dk ** -0.5
+    y = [f64(t) for t in x]
+    want = ref.forward(*y[:4], y[4], None, sc) + ref.backward(*y[:4], y[5], y[4], y[6], None, sc)
+    rows = (np.abs(np.repeat(y[0], H, 2)) * np.repeat(want[2][1], H, 2)).sum(3)
+    rows = rows + (np.abs(np.repeat(y[1], H, 2)) * np.repeat(want[3][1], H, 2)).sum(3)
+    want[5][1][:] += n ** 0.5 * rows.max(1, keepdims=True)
+    for name, a, w in zip(("o", "ht", "dq", "dk", "dv", "dg", "dh0"), (o, ht) + tuple(grads), want):
+        last = a[1:] if name in ("ht", "dh0") else a[:, T - n:]
+        close(last, w, name, n, Dk, Dv, "bf16")
+    assert not o[:, :T - n].any() and not ht[0].any()

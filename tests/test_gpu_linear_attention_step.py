@@ -163,3 +163,19 @@ def test_prompt_then_steps(m):
     fp32 = (8 * T + 2 * D + 256) * 2.0 ** -24
     assert np.all(np.abs(f64(o) - want) <= (fp32 + 2.0 ** -17) * mag + 2.0 ** -8 * np.abs(want))
     assert np.all(np.abs(f64(state) - wh) <= fp32 * hm)
+
+
+def test_states_past_32_bits(m):
+    """A pool of more than 2^32 elements: only the states of the batch are touched."""
+    B, H, D = 3, 16, 128
+    pool = 2 ** 32 // (H * D * D) + 5
+    q, k, v, g, some = make(31, B, B, H, H, D, D)
+    state = torch.empty(pool, H, D, D, device=DEV)
+    slots = [pool - 1, 0, pool - 3]
+    at = torch.tensor(slots, dtype=torch.int32, device=DEV)
+    state[at.long()] = some
+    state[pool - 2] = 7.0
+    o = m.linear_attention_step(q, k, v, g, state, slots=at)
+    want = some.clone()
+    near = m.linear_attention_step(q, k, v, g, want)
+    assert torch.equal(o, near) and torch.equal(state[at.long()], want) and bool((state[pool - 2] == 7.0).all())

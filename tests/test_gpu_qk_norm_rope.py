@@ -182,3 +182,22 @@ def test_empty(m):
     w = torch.ones(64, device=DEV)
     assert m.qk_norm_rope_fwd(q, q, w, w)[0].shape == q.shape
     assert torch.equal(m.qk_norm_rope_bwd(q, q, w, w, None, None, q, q)[2], torch.zeros_like(w))
+
+
+def test_offsets_past_32_bits(m):
+    """Rows of more than 2^31 elements: the last tokens against the same ones by themselves."""
+    T, n, H, D = 2 ** 17 + 9, 9, 128, 128
+    assert (T - n) * H * D >= 2 ** 31
+    gen = torch.Generator(device=DEV)
+    gen.manual_seed(3)
+    q = torch.zeros(1, T, H, D, dtype=torch.bfloat16, device=DEV)
+    k = torch.zeros(1, T, 1, D, dtype=torch.bfloat16, device=DEV)
+    for x in (q, k):
+        x[:, T - n:] = torch.randn(1, n, x.shape[2], D, device=DEV, generator=gen).bfloat16()
+    w = torch.rand(D, device=DEV, generator=gen)
+    near = [x[:, T - n:].contiguous() for x in (q, k)]
+    for a, b in zip(m.qk_norm_rope_fwd(q, k, w, w), m.qk_norm_rope_fwd(*near, w, w)):
+        assert torch.equal(a[:, T - n:], b) and not a[:, :T - n].any()
+    far, by = m.qk_norm_rope_bwd(q, k, w, w, None, None, q, k), m.qk_norm_rope_bwd(*near, w, w, None, None, *near)
+    for a, b in zip(far[:2], by[:2]):
+        assert torch.equal(a[:, T - n:], b) and not a[:, :T - n].any()
