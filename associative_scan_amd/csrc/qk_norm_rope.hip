@@ -7,9 +7,11 @@
 // row (one head of one token) is spread over L = 8, 16 or 32 lanes of 8 elements,
 // two units of 4. A rotated lane holds both halves of its four pairs, (4 c + i,
 // rot / 2 + 4 c + i), so the rotation needs nothing from other lanes and a pair
-// shares its angle; 16 lanes still read 128 contiguous bytes at a time. A lane
-// group takes several heads of a token and reads the token's angles once. Loads
-// and stores are streaming: they pass the caches by for inputs that come back.
+// shares its angle. A lane's 16 bytes of a 16-bit type are one access: of the
+// first half by even lanes, of the second by odd ones, and two neighbours then
+// exchange a unit. A lane group takes several heads of a token and reads the
+// token's angles once. Loads and stores are streaming: they pass the caches by for
+// inputs that come back.
 // Measured in bf16, D = 128: forward, 32767 tokens of 16 + 4 heads 76 us (4.5
 // TB/s), forward and backward, 32768 tokens of 12 + 12 heads 191 us (5.3 TB/s; a
 // copy reaches 5.35); a decoding step of 7 tokens 4.4 us, its three dependent trips
@@ -27,11 +29,6 @@ struct Four {
 template <class T>
 __device__ __forceinline__ f4v wide(T v) {
   return __builtin_convertvector(v, f4v);
-}
-template <class T>
-__device__ __forceinline__ void store4(T* p, f4v v) {
-  typedef typename Four<T>::type t4;
-  __builtin_nontemporal_store(__builtin_convertvector(v, t4), (t4*)p);
 }
 __device__ __forceinline__ f4v load_weight(const void* w, int dtype, int at) {
   f4v v = {1.f, 1.f, 1.f, 1.f};
@@ -67,6 +64,8 @@ __device__ __forceinline__ float dot4(f4v a, f4v b) { return (a[0] * b[0] + a[1]
 // none). Interleaved pairs lie inside a unit.
 struct Place {
   int a, b;
+  int at;         // the 8 elements that the lane itself reads and writes, of a 16-bit type
+  bool even, odd; // place in a pair of lanes that exchange a unit
   bool in, rotated;
 };
 template <bool PAIRS>
@@ -76,7 +75,21 @@ __device__ __forceinline__ Place place_of(const NormProblem& p, int lane) {
   q.rotated = lane * 8 < p.rot;
   q.a = q.rotated && !PAIRS ? lane * 4 : lane * 8;
   q.b = q.rotated && !PAIRS ? p.rot / 2 + lane * 4 : lane * 8 + 4;
+  q.even = q.rotated && !PAIRS && !(lane & 1);
+  q.odd = q.rotated && !PAIRS && (lane & 1);
+  q.at = q.odd ? p.rot / 2 + (lane - 1) * 4 : q.a;
   return q;
+}
+// An even lane's second unit and the next one's first change places.
+__device__ __forceinline__ u4v exchange(u4v x, const Place& at) {
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const uint32_t mine = at.odd ? x[i] : x[2 + i];
+    const uint32_t other = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)mine, 0xb1, 0xf, 0xf, false);  // lane ^ 1
+    x[i] = at.odd ? other : x[i];
+    x[2 + i] = at.even ? other : x[2 + i];
+  }
+  return x;
 }
 struct Angles {
   f4v c, s;
@@ -129,17 +142,41 @@ struct Rows {
 template <class TIn, int HP>
 struct Heads4 {
   typedef typename Four<TIn>::type t4;
-  t4 u[HP], v[HP];
+  static constexpr int W = sizeof(TIn) == 4 ? 2 : 1;  // 16-byte accesses
+  u4v w[HP][W];
   __device__ __forceinline__ void load(const Heads& x, int64_t b, int64_t t, int h0, int nh, const Place& at) {
     const TIn* p = (const TIn*)x.p + b * x.sb + t * x.st + h0 * x.sh;
 #pragma unroll
     for (int j = 0; j < HP; ++j) {
-      u[j] = t4{0, 0, 0, 0};
-      v[j] = t4{0, 0, 0, 0};
+#pragma unroll
+      for (int i = 0; i < W; ++i) w[j][i] = u4v{0, 0, 0, 0};
       if (at.in && j < nh) {
-        u[j] = __builtin_nontemporal_load((const t4*)(p + j * x.sh + at.a));
-        v[j] = __builtin_nontemporal_load((const t4*)(p + j * x.sh + at.b));
+        w[j][0] = __builtin_nontemporal_load((const u4v*)(p + j * x.sh + (W == 2 ? at.a : at.at)));
+        if constexpr (W == 2) w[j][1] = __builtin_nontemporal_load((const u4v*)(p + j * x.sh + at.b));
       }
+    }
+  }
+  // the units at at.a and at.b; by all lanes of a wave
+  __device__ __forceinline__ void get(int j, const Place& at, f4v& u, f4v& v) const {
+    if constexpr (W == 2) {
+      u = __builtin_bit_cast(f4v, w[j][0]);
+      v = __builtin_bit_cast(f4v, w[j][1]);
+    } else {
+      const u4v x = exchange(w[j][0], at);
+      u = wide(__builtin_bit_cast(t4, u2v{x[0], x[1]}));
+      v = wide(__builtin_bit_cast(t4, u2v{x[2], x[3]}));
+    }
+  }
+  static __device__ __forceinline__ void put(TIn* p, const Place& at, bool live, f4v a, f4v b) {
+    if constexpr (W == 2) {
+      if (!live) return;
+      __builtin_nontemporal_store(a, (f4v*)(p + at.a));
+      __builtin_nontemporal_store(b, (f4v*)(p + at.b));
+    } else {
+      const u2v x = __builtin_bit_cast(u2v, __builtin_convertvector(a, t4));
+      const u2v y = __builtin_bit_cast(u2v, __builtin_convertvector(b, t4));
+      const u4v z = exchange(u4v{x[0], x[1], y[0], y[1]}, at);
+      if (live) __builtin_nontemporal_store(z, (u4v*)(p + at.at));
     }
   }
 };
@@ -188,14 +225,12 @@ __global__ __launch_bounds__(256) void k_norm_fwd(const NormProblem p, const Nor
     TIn* yp = (TIn*)x.y + ((r.b * p.T + r.t) * x.heads + r.h0) * p.D;
 #pragma unroll
     for (int j = 0; j < HP; ++j) {
-      const f4v u = wide(now.u[j]), v = wide(now.v[j]);
+      f4v u, v;
+      now.get(j, at, u, v);
       const float rs = rsqrtf(row_sum<L>(dot4(u, u) + dot4(v, v)) * inv + p.eps);
       f4v a = u * rs * wu, b = v * rs * wv;
       rotate<PAIRS>(a, b, turn, 1.f);
-      if (at.in && j < r.nh) {
-        store4<TIn>(yp + (int64_t)j * p.D + at.a, a);
-        store4<TIn>(yp + (int64_t)j * p.D + at.b, b);
-      }
+      Heads4<TIn, HP>::put(yp + (int64_t)j * p.D, at, at.in && j < r.nh, a, b);
     }
     r = next;
   }
@@ -248,20 +283,18 @@ __global__ __launch_bounds__(256) void k_norm_bwd(const NormProblem p, const Nor
     TIn* yp = (TIn*)x.y + ((r.b * p.T + r.t) * x.heads + r.h0) * p.D;
 #pragma unroll
     for (int j = 0; j < HP; ++j) {
-      f4v a = wide(dnow.u[j]), b = wide(dnow.v[j]);
+      f4v a, b, u, v;
+      dnow.get(j, at, a, b);
       rotate<PAIRS>(a, b, turn, -1.f);
-      const f4v u = wide(now.u[j]), v = wide(now.v[j]);
+      now.get(j, at, u, v);
       const float rs = rsqrtf(row_sum<L>(dot4(u, u) + dot4(v, v)) * inv + p.eps);
       const f4v hu = u * rs, hv = v * rs, tu = a * wu, tv = b * wv;
       const float m = row_sum<L>(dot4(tu, hu) + dot4(tv, hv)) * inv;
       if (j < r.nh) {
         du += a * hu;
         dv += b * hv;
-        if (at.in) {
-          store4<TIn>(yp + (int64_t)j * p.D + at.a, (tu - hu * m) * rs);
-          store4<TIn>(yp + (int64_t)j * p.D + at.b, (tv - hv * m) * rs);
-        }
       }
+      Heads4<TIn, HP>::put(yp + (int64_t)j * p.D, at, at.in && j < r.nh, (tu - hu * m) * rs, (tv - hv * m) * rs);
     }
     r = next;
   }
