@@ -2,11 +2,13 @@
 //
 // S = e^g S + k v^T in place and o = scale S^T q. The state is read and written
 // once (8 Dk Dv bytes per head) and everything else is small, so the step is
-// bound by HBM; one workgroup per head and COLS columns of its state, every
-// thread holding its part in registers between the read and the write. A row of
-// COLS fp32 columns is read as whole 16-byte units, 128 bytes at a time, past the
-// caches: a pool of states is larger than they are. 251 sequences of 12 heads,
-// 128 x 128: 395 MB in 79 us, 5.0 TB/s (a copy reaches 5.35). One sequence: 4.4 us,
+// bound by HBM: one workgroup per head (or per half or quarter of its columns where
+// there are few), every thread holding its part in registers between the read and
+// the write, past the caches: a pool of states is larger than they are. Read as one
+// stretch of memory, since pieces of rows that end inside a 128-byte line cost as
+// much as whole ones: 400 sequences of 12 heads take 29 us at 40 x 72 and 83 us at
+// 96 x 112, cut into columns of 32 they took 55 and 117. 251 sequences of 12 heads,
+// 128 x 128: 395 MB in 77 us, 5.1 TB/s (a copy reaches 5.35). One sequence: 4.6 us,
 // the latency of a launch and of two trips to memory.
 #include "la_device.hpp"
 
@@ -18,45 +20,40 @@ __device__ __forceinline__ float widen(TIn x) {
   return (float)x;
 }
 
-// Sequence of batch row b whose state slot it owns: -1 when the slot is out of
-// range, or when an earlier row of the batch has the same slot (that row then
-// runs this one's step after its own, in the order of the batch).
-__device__ __forceinline__ bool slot_taken_before(const int32_t* slots, int b, int32_t slot) {
-  bool hit = false;
-  for (int i = (int)threadIdx.x; i < b; i += (int)blockDim.x) hit |= slots[i] == slot;
-  return __syncthreads_or(hit);
+// Rows that share a slot are run by the first of them, in the order of the batch.
+// The thread's part of the search for row b's slot among the other rows: -1 when
+// an earlier row has it, else the next one that does, or n.
+__device__ __forceinline__ int search(const int32_t* slots, int first, int b, int n, int32_t slot) {
+  int found = n;
+  for (int i = first + (int)threadIdx.x; i < n; i += (int)blockDim.x)
+    if (slots[i] == slot && i != b) found = i < b ? -1 : (i < found ? i : found);
+  return found;
 }
-// The next row after b with the same slot, or n.
-__device__ __forceinline__ int next_with(const int32_t* slots, int b, int n, int32_t slot, int* lds) {
-  __syncthreads();
-  if (threadIdx.x == 0) *lds = n;
-  __syncthreads();
-  int first = n;
-  for (int i = b + 1 + (int)threadIdx.x; i < n; i += (int)blockDim.x)
-    if (slots[i] == slot) {
-      first = i;
-      break;
-    }
-  if (first < n) atomicMin(lds, first);
-  __syncthreads();
-  return *lds;
+// The least over a wave, to its lane 0.
+__device__ __forceinline__ int wave_min(int x) {
+#pragma unroll
+  for (int m = 32; m; m >>= 1) {
+    const int y = __shfl_xor(x, m);
+    x = y < x ? y : x;
+  }
+  return x;
 }
 
-// COLS columns by DK rows on 256 threads: 16-byte units of a row by rows.
-template <class TIn, int DK, int COLS>
-__global__ __launch_bounds__(256) void k_attn_step(const StepArgs a) {
-  constexpr int UN = COLS / 4;       // units of a row
-  constexpr int RW = 256 / UN;       // rows at a time
-  constexpr int N = DK / RW;         // rows of a thread
-  static_assert(DK % RW == 0, "rows");
-  __shared__ float qs[DK], ks[DK];
-  __shared__ __align__(16) f4v part[4][UN];
-  __shared__ int next;
-  const int tid = threadIdx.x, u = tid % UN, r0 = tid / UN;
-  const int parts = (a.Dv + COLS - 1) / COLS;
+// `cols` columns of a head's state on 256 threads: cols / 4 units of 16 bytes by
+// as many rows at a time as fit, up to N times. A whole state's rows are one
+// stretch of memory, whatever their length.
+template <class TIn, int N>
+__global__ __launch_bounds__(256) void k_attn_step(const StepArgs a, const int cols) {
+  constexpr int DK = 128;
+  __shared__ float qs[DK + 1], ks[DK + 1];  // zeros past Dk
+  __shared__ __align__(16) f4v part[256];
+  __shared__ int found[4];
+  const int units = cols / 4, RW = 256 / units;
+  const int tid = threadIdx.x, r0 = tid / units, u = tid - r0 * units;
+  const int parts = a.Dv / cols;
   const int part_i = blockIdx.x % parts, h = blockIdx.x / parts % a.H, b0 = blockIdx.x / parts / a.H;
-  const int col = part_i * COLS + u * 4;
-  const bool in = col < a.Dv;
+  const int col = part_i * cols + u * 4;
+  const bool in = r0 < RW;
   const int32_t slot = a.slots ? a.slots[b0] : b0;
   const bool live = slot >= 0 && slot < a.pool;
   // a row's own inputs, one entry of q and k to a thread
@@ -83,42 +80,57 @@ __global__ __launch_bounds__(256) void k_attn_step(const StepArgs a) {
     S[i] = f4v{0.f, 0.f, 0.f, 0.f};
     if (live && in && row < a.Dk) S[i] = __builtin_nontemporal_load((const f4v*)(sp + (int64_t)row * a.Dv));
   }
+  if (!live) {  // no state: a zero output
+    TIn* op = (TIn*)a.o + ((int64_t)b0 * a.H + h) * a.Dv;
+    if (r0 == 0 && in)
+      for (int j = 0; j < 4; ++j) op[col + j] = (TIn)0.f;
+    return;
+  }
   // the loads above are in flight; what is read of a state another row owns is dropped
-  if (a.slots && live && slot_taken_before(a.slots, b0, slot)) return;
-  for (int b = b0; b < a.B;) {
+  int next = wave_min(a.slots ? search(a.slots, 0, b0, a.B, slot) : a.B);
+  for (int b = b0;;) {
     TIn* op = (TIn*)a.o + ((int64_t)b * a.H + h) * a.Dv;
-    if (!live) {  // no state: a zero output
-      if (r0 == 0 && in)
-        for (int j = 0; j < 4; ++j) op[col + j] = (TIn)0.f;
-      return;
-    }
-    if (tid < DK) {
+    if ((tid & 63) == 0) found[tid >> 6] = next;
+    if (tid <= DK) {
       qs[tid] = qv;
       ks[tid] = kv;
     }
     const float decay = exp2_fast((float)log2_decay(gv));
     __syncthreads();
+    next = found[0];
+#pragma unroll
+    for (int w = 1; w < 4; ++w) next = found[w] < next ? found[w] : next;
+    if (next < 0) return;
     f4v o = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int row = r0 + i * RW;
+      const int row = r0 + i * RW < DK ? r0 + i * RW : DK;
       S[i] = S[i] * decay + v * ks[row];
       o += S[i] * qs[row];
     }
-    // rows of a wave, then waves
+    // the sums of a wave's rows first where its lanes hold whole ones
+    int sums = RW;
+    if ((units & (units - 1)) == 0) {
+      sums = 4;
+      for (int m = units; m < 64; m <<= 1)
 #pragma unroll
-    for (int m = UN; m < 64; m <<= 1)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) o[j] += __shfl_xor(o[j], m);
-    if ((tid & 63) < UN) part[tid >> 6][u] = o;
+        for (int j = 0; j < 4; ++j) o[j] += __shfl_xor(o[j], m);
+      if ((tid & 63) < units) part[(tid >> 6) * units + u] = o;
+    } else {
+      part[tid] = o;
+    }
     __syncthreads();
-    if (tid < UN && in) {
-      o = part[0][u] + part[1][u] + part[2][u] + part[3][u];
+    if (tid < units) {
+      o = part[tid];
+#pragma unroll 4
+      for (int i = 1; i < sums; ++i) o += part[i * units + tid];
 #pragma unroll
       for (int j = 0; j < 4; ++j) op[col + j] = (TIn)o[j];
     }
-    b = a.slots ? next_with(a.slots, b, a.B, slot, &next) : a.B;
-    if (b < a.B) fetch(b);
+    if (next >= a.B) break;
+    b = next;
+    fetch(b);
+    next = wave_min(search(a.slots, b + 1, b, a.B, slot));
   }
 #pragma unroll
   for (int i = 0; i < N; ++i) {
@@ -127,14 +139,23 @@ __global__ __launch_bounds__(256) void k_attn_step(const StepArgs a) {
   }
 }
 
+template <class TIn, int N>
+static hipError_t step_rows(const StepArgs& a, int cols, hipStream_t st) {
+  const unsigned blocks = (unsigned)((int64_t)a.B * a.H * (a.Dv / cols));
+  hipLaunchKernelGGL((k_attn_step<TIn, N>), dim3(blocks), dim3(256), 0, st, a, cols);
+  return hipGetLastError();
+}
 template <class TIn>
 static hipError_t step_type(const StepArgs& a, hipStream_t st) {
-  const unsigned heads = (unsigned)((int64_t)a.B * a.H);
-  if (a.Dk <= 64)
-    hipLaunchKernelGGL((k_attn_step<TIn, 64, 32>), dim3(heads * ((a.Dv + 31) / 32)), dim3(256), 0, st, a);
-  else
-    hipLaunchKernelGGL((k_attn_step<TIn, 128, 32>), dim3(heads * ((a.Dv + 31) / 32)), dim3(256), 0, st, a);
-  return hipGetLastError();
+  // few heads: halves and quarters of a state, in whole 128-byte lines, until every
+  // CU has two workgroups
+  int cols = a.Dv;
+  while (cols % 64 == 0 && (int64_t)a.B * a.H * (a.Dv / cols) < 512) cols /= 2;
+  const int rows = 256 / (cols / 4), n = (a.Dk + rows - 1) / rows;
+  if (n <= 4) return step_rows<TIn, 4>(a, cols, st);
+  if (n <= 8) return step_rows<TIn, 8>(a, cols, st);
+  if (n <= 12) return step_rows<TIn, 12>(a, cols, st);
+  return step_rows<TIn, 16>(a, cols, st);
 }
 
 hipError_t launch_step(const StepArgs& a, int dtype, hipStream_t st) {
