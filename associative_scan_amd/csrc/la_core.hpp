@@ -19,6 +19,11 @@ constexpr int kPiecesP = kPlanes<T> == 3 ? 3 : 2;
 template <class T, bool EXACT>
 constexpr int kPiecesS = EXACT || kPlanes<T> == 3 ? 3 : 2;
 constexpr int kPiecesZ = 3;
+// Chunks whose decays are computed at a time, each by one of NW waves: all of them
+// where LDS has the room, two for fp32's three planes (two workgroups of 128 x 128
+// to a CU leave them 2 KB).
+template <class T, int NW>
+constexpr int kDecays = kPlanes<T> == 3 ? 2 : NW;
 
 // A lane's offsets into the tiles (see la_device.hpp).
 template <int C, int DX, int DZ>
@@ -515,7 +520,7 @@ __device__ __forceinline__ float load_gate(const float* g, int64_t st, int t0, i
 }
 
 // The decays of a span's chunks, in the order they run (REV: from the last). A
-// prefix sum in 64 bits is a chain of a few hundred cycles: each of the WAVES
+// prefix sum in 64 bits is a chain of a few hundred cycles: each of WAVES waves
 // takes a chunk of its own, so that a workgroup waits for one such chain in WAVES
 // chunks, and g is read that far ahead.
 template <int C, int WAVES, bool REV>
@@ -534,12 +539,12 @@ struct SpanDecays {
   __device__ __forceinline__ void read() {
     const int i = next + wave;
     next += WAVES;
-    ahead = i < chunks ? load_gate(g, st, (REV ? chunks - 1 - i : i) * C, n) : 0.f;
+    ahead = wave < WAVES && i < chunks ? load_gate(g, st, (REV ? chunks - 1 - i : i) * C, n) : 0.f;
   }
   // Those of the next WAVES chunks. Barriers on both sides: the last ones' must
   // have been read, and these not yet be.
   __device__ __forceinline__ void write() {
-    total += write_decays<C, REV>(dec[wave], ahead, scale);
+    if (wave < WAVES) total += write_decays<C, REV>(dec[wave], ahead, scale);
     read();
   }
 };
@@ -554,12 +559,12 @@ struct SpanTiles {
   static constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>;
   bf16 Y[PL * C * DX];
   bf16 Z[PL * C * NW * 32];
-  Decays<C> dec[NW];
-  double sums[NW];
+  Decays<C> dec[kDecays<TIn, NW>];
+  double sums[kDecays<TIn, NW>];
 };
 template <class TIn, int DX, int NW, bool REV>
 __device__ __forceinline__ void span_state(const LaProblem& pr, const Between& a, SpanTiles<TIn, DX, NW>& sh) {
-  constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, DZ = NW * 32, NT = NW * 64;
+  constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, DZ = NW * 32, NT = NW * 64, G = kDecays<TIn, NW>;
   const Heads &y = a.y, &z = a.z;
   const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
@@ -577,7 +582,7 @@ __device__ __forceinline__ void span_state(const LaProblem& pr, const Between& a
   // loads run two chunks ahead: a chunk's own work is shorter than a load
   TileRegs<TIn, C, DX, NT> ry[2];
   TileRegs<TIn, C, DZ, NT> rz[2];
-  SpanDecays<C, NW, REV> decays(sh.dec, gp, pr.gst, sp.n, a.sz, wave);
+  SpanDecays<C, G, REV> decays(sh.dec, gp, pr.gst, sp.n, a.sz, wave);
   const LaneOffsets<C, DX, DZ> at(z0);
   f16v none[C / 32];
   const auto fetch = [&](int i, int s) {
@@ -588,10 +593,10 @@ __device__ __forceinline__ void span_state(const LaProblem& pr, const Between& a
   const auto chunk = [&](int i, int s) {
     ry[s].store(sh.Y);
     rz[s].store(sh.Z);
-    if (i % NW == 0) decays.write();
+    if (i % G == 0) decays.write();
     __syncthreads();
     if (i + 2 < nc) fetch(i + 2, s);
-    within_chunk<PL, C, DX, DZ, 0, REV>(sh.Y, sh.Z, nullptr, sh.dec[i % NW], at, S, none);
+    within_chunk<PL, C, DX, DZ, 0, REV>(sh.Y, sh.Z, nullptr, sh.dec[i % G], at, S, none);
     __syncthreads();
   };
   fetch(0, 0);
@@ -601,11 +606,11 @@ __device__ __forceinline__ void span_state(const LaProblem& pr, const Between& a
     if (i + 1 < nc) chunk(i + 1, 1);
   }
   store_state<DX>(S, a.states + ((int64_t)slot * pr.H + h) * pr.Dk * pr.Dv, pr.Dv, 1, pr.Dk, pr.Dv, z0);
-  if (lane_id() == 0) sh.sums[wave] = decays.total;
+  if (wave < G && lane_id() == 0) sh.sums[wave] = decays.total;
   __syncthreads();
   if (tid == 0) {
     double total = 0.0;
-    for (int w = 0; w < NW; ++w) total += sh.sums[w];
+    for (int w = 0; w < G; ++w) total += sh.sums[w];
     a.totals[(int64_t)slot * pr.H + h] = exp2_fast((float)total);
   }
 }

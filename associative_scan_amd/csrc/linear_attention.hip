@@ -28,7 +28,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   __shared__ __align__(16) bf16 K[PL * C * DX];
   __shared__ __align__(16) bf16 V[PL * C * DZ];
   __shared__ __align__(16) bf16 P[NP * C * C];
-  __shared__ __align__(16) Decays<C> dec[NW];
+  constexpr int G = kDecays<TIn, NW>;
+  __shared__ __align__(16) Decays<C> dec[G];
   const LaProblem& pr = a.pr;
   const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
   const int h = blockIdx.x % pr.H, slot = blockIdx.x / pr.H;
@@ -51,7 +52,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
   const float* gp = gate_base(pr, sp.batch, sp.t0, h);
   TileRegs<TIn, C, DX, NT> rq, rk;
   TileRegs<TIn, C, DZ, NT> rv;
-  SpanDecays<C, NW, false> decays(dec, gp, pr.gst, sp.n, pr.scale, wave);
+  SpanDecays<C, G, false> decays(dec, gp, pr.gst, sp.n, pr.scale, wave);
   // the next chunk's loads are issued in three places: all at once they hold up
   // the waves for as long as the memory pipeline takes to accept them
   const auto fetch_q = [&](int t) { rq.load(qp + (int64_t)t * a.q.st, a.q.st, pr.Dk, sp.n - t); };
@@ -89,7 +90,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_fwd(const FwdArgs a) {
       rq.store(Q);
       rk.store(K);
       rv.store(V);
-      if (++cur == NW) {
+      if (++cur == G) {
         cur = 0;
         decays.write();
       }
@@ -151,17 +152,20 @@ __global__ __launch_bounds__(256) void k_join(const LaProblem pr, const Between 
 // Steps per span. A workgroup per head and sequence needs no second pass over
 // k and v, but fills the card only with many heads and sequences; with fewer the
 // time axis is cut. What a cut costs, in steps of the main pass: its spans one
-// after the other in as many rounds as the card's 512 places ask for (a workgroup
-// with a CU of its own runs faster, 5 us for 64 bf16 steps against 8 us where two
-// share one), a round's start, the pass that gives the spans' own states (0.45 of
-// the forward kernel's time, 0.3 of the backward's), and the joins and launches,
-// some 10 us, which are fewer steps the longer a step takes.
+// after the other in as many rounds as the card's places ask for (two workgroups to
+// a CU; three where a state has at most 64 x 64, or in fp16 64 rows or columns: 8 x
+// 4096 steps of 12 heads of 64 take 87 us then, planned for two 116; a workgroup with a CU of its own runs
+// faster, 5 us for 64 bf16 steps of 128 x 128 against 8 us where two share one), a
+// round's start, the pass that gives the spans' own states (0.45 of the forward
+// kernel's time, 0.3 of the backward's), and the joins and launches, some 10 us,
+// which are fewer steps the longer a step takes.
 void plan(LaProblem& p, int dtype, bool backward) {
-  const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H;
+  const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H, small = (p.Dk <= 64) + (p.Dv <= 64);
+  const int64_t places = small == 2 || (small == 1 && dtype == 2) ? 768 : 512;
   const double states = backward ? 1.3 : 1.45, fixed = (dtype == 1 ? 128 : 80) * (backward ? 0.6 : 1.0);
   const auto cost = [&](int64_t span) {
     const int64_t n = (p.T + span - 1) / span, blocks = n * rows;
-    const int64_t rounds = (blocks + 511) / 512;
+    const int64_t rounds = (blocks + places - 1) / places;
     const double step = blocks <= 256 ? 0.62 : 1.0;
     const double run = rounds * step * ((double)(span < p.T ? span : p.T) + 48);
     return n == 1 ? run : states * run + fixed + 3.0 * n;

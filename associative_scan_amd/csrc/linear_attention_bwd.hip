@@ -39,7 +39,8 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   __shared__ __align__(16) bf16 V[PL * C * DX];
   __shared__ __align__(16) bf16 K[PL * C * DZ];
   __shared__ __align__(16) bf16 P[NP * C * C];
-  __shared__ __align__(16) Decays<C> dec[NW];
+  constexpr int G = kDecays<TIn, NW>;
+  __shared__ __align__(16) Decays<C> dec[G];
   __shared__ float part[NW][C];
   const LaProblem& pr = a.pr;
   const int tid = threadIdx.x, wave = wave_id(), z0 = wave * 32;
@@ -69,7 +70,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
   const float* gp = gate_base(pr, sp.batch, sp.t0, h);
   TileRegs<TIn, C, DX, NT> ro, rv;
   TileRegs<TIn, C, DZ, NT> rk;
-  SpanDecays<C, NW, false> decays(dec, gp, pr.gst, sp.n, pr.scale, wave);
+  SpanDecays<C, G, false> decays(dec, gp, pr.gst, sp.n, pr.scale, wave);
   const auto fetch_o = [&](int t) { ro.load(op + (int64_t)t * a.dO.st, a.dO.st, pr.Dv, sp.n - t); };
   const auto fetch_v = [&](int t) { rv.load(vp + (int64_t)t * a.v.st, a.v.st, pr.Dv, sp.n - t); };
   const auto fetch_k = [&](int t) { rk.load(kp + (int64_t)t * a.k.st, a.k.st, pr.Dk, sp.n - t); };
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(NW * 64, 2) void k_attn_dq(const BwdArgs a) {
       ro.store(O);
       rv.store(V);
       rk.store(K);
-      if (++cur == NW) {
+      if (++cur == G) {
         cur = 0;
         decays.write();
       }
@@ -154,7 +155,7 @@ struct DkvTiles {
   bf16 V[PL * C * DV];  // and then the chunk's dv
   bf16 O[PL * C * DV];
   bf16 P[2][kPiecesP<TIn> * C * C];
-  Decays<C> dec[(DK + DV) / 32];
+  Decays<C> dec[kDecays<TIn, (DK + DV) / 32>];
   float part[DK / 32][C];
   float sums[kTiles<C>][2][16];
 };
@@ -164,6 +165,7 @@ __device__ __forceinline__ void dkv_span(const BwdArgs& a, const Span& sp, int s
   constexpr int PL = kPlanes<TIn>, C = kChunk<TIn>, NK = DK / 32, NV = DV / 32, NW = NK + NV, NT = (IS_DK ? NK : NV) * 64,
                 NP = kPiecesP<TIn>, DX = IS_DK ? DV : DK, DZ = IS_DK ? DK : DV, NS = IS_DK ? kPiecesS<TIn, DG> : kPiecesS<TIn, false>,
                 NZ = IS_DK ? kPiecesZ : kPiecesS<TIn, false>;
+  constexpr int G = kDecays<TIn, NW>;
   constexpr bool GATE = IS_DK && DG;
   const LaProblem& pr = a.pr;
   const int tid = threadIdx.x, wave = wave_id(), z0 = (IS_DK ? wave - NV : wave) * 32;
@@ -188,7 +190,7 @@ __device__ __forceinline__ void dkv_span(const BwdArgs& a, const Span& sp, int s
   const TIn* p2 = head_base<TIn>(h2, sp.batch, sp.t0, h);
   const float* gp = gate_base(pr, sp.batch, sp.t0, h);
   TileRegs<TIn, C, DZ, NT> r1, r2;
-  SpanDecays<C, NW, true> decays(sh.dec, gp, pr.gst, sp.n, pr.scale, wave);
+  SpanDecays<C, G, true> decays(sh.dec, gp, pr.gst, sp.n, pr.scale, wave);
   const auto fetch1 = [&](int t) { r1.load(p1 + (int64_t)t * h1.st, h1.st, dz, sp.n - t); };
   const auto fetch2 = [&](int t) { r2.load(p2 + (int64_t)t * h2.st, h2.st, dz, sp.n - t); };
   const LaneOffsets<C, DX, DZ> at(z0);
@@ -275,7 +277,7 @@ __device__ __forceinline__ void dkv_span(const BwdArgs& a, const Span& sp, int s
     if (more) {
       r1.store(T1);
       r2.store(T2);
-      if (++cur == NW) {
+      if (++cur == G) {
         cur = 0;
         decays.write();
       }
