@@ -12,10 +12,10 @@
 // exchange a unit. A lane group takes several heads of a token and reads the
 // token's angles once. Loads and stores are streaming: they pass the caches by for
 // inputs that come back.
-// Measured in bf16, D = 128: forward, 32767 tokens of 16 + 4 heads 76 us (4.5
-// TB/s), forward and backward, 32768 tokens of 12 + 12 heads 191 us (5.3 TB/s; a
-// copy reaches 5.35); a decoding step of 7 tokens 4.4 us, its three dependent trips
-// to memory.
+// Measured in bf16, D = 128: forward, 32767 tokens of 16 + 4 heads 61 us (5.6 TB/s;
+// with two accesses of 8 bytes 76), forward and backward, 32768 tokens of 12 + 12
+// heads 189 us (5.5 TB/s; a copy reaches 5.35); a decoding step of 7 tokens 4.4 us,
+// its three dependent trips to memory.
 #include "la_device.hpp"
 #include "qk_norm_rope.hpp"
 
@@ -370,7 +370,7 @@ static hipError_t fwd_heads(const NormProblem& p, const NormSide& q, const NormS
 template <class TIn, int L, bool PAIRS>
 static hipError_t fwd_lanes(const NormProblem& p, const NormSide& q, const NormSide& k, hipStream_t st) {
   // four heads per lane group once there is a wave for every SIMD of the card
-  // (32767 tokens of 16 + 4 heads: 77 us, with two 82 us, with one 95 us)
+  // (32767 tokens of 16 + 4 heads: 62 us, with two 67 us; below, one gives the most waves)
   return p.B * p.T * (q.heads + k.heads) * L >= (int64_t)1024 * 64 * 4 ? fwd_heads<TIn, L, 4, PAIRS>(p, q, k, st)
                                                                        : fwd_heads<TIn, L, 1, PAIRS>(p, q, k, st);
 }
