@@ -154,15 +154,17 @@ __global__ __launch_bounds__(256) void k_join(const LaProblem pr, const Between 
 // time axis is cut. What a cut costs, in steps of the main pass: its spans one
 // after the other in as many rounds as the card's places ask for (two workgroups to
 // a CU; three where a state has at most 64 x 64, or in fp16 64 rows or columns: 8 x
-// 4096 steps of 12 heads of 64 take 87 us then, planned for two 116; a workgroup with a CU of its own runs
-// faster, 5 us for 64 bf16 steps of 128 x 128 against 8 us where two share one), a
-// round's start, the pass that gives the spans' own states (0.45 of the forward
-// kernel's time, 0.3 of the backward's), and the joins and launches, some 10 us,
-// which are fewer steps the longer a step takes.
+// 4096 steps of 12 heads of 64 take 87 us then, planned for two 116; a workgroup
+// with a CU of its own runs faster, 5 us for 64 bf16 steps of 128 x 128 against 8 us
+// where two share one), a round's start, the pass that gives the spans' own states
+// (0.45 of the forward kernel's time, 0.3 of the backward's), and the joins and
+// launches, the fewer steps the longer these are (training passes of 2 x 130 steps,
+// 12 heads of 128 in bf16: 67 us cut, 76 uncut; of 2 x 200: 77 and 92; prompts of
+// 250 steps: 21.5 and 23.4 us).
 void plan(LaProblem& p, int dtype, bool backward) {
   const int64_t rows = (p.cu ? 1 : p.B) * (int64_t)p.H, small = (p.Dk <= 64) + (p.Dv <= 64);
   const int64_t places = small == 2 || (small == 1 && dtype == 2) ? 768 : 512;
-  const double states = backward ? 1.3 : 1.45, fixed = (dtype == 1 ? 128 : 80) * (backward ? 0.6 : 1.0);
+  const double states = backward ? 1.3 : 1.45, fixed = backward ? 8 : dtype == 1 ? 60 : 30;
   const auto cost = [&](int64_t span) {
     const int64_t n = (p.T + span - 1) / span, blocks = n * rows;
     const int64_t rounds = (blocks + places - 1) / places;
